@@ -62,8 +62,9 @@ int64_t jl_group_size(int64_t L, int64_t w_pretrained);
 
 /* Synchronises `stream`, then returns and clears the device status word:
  * JL_OK; JL_ERR_TIMEOUT if a bounded wait ran out; JL_ERR_INVALID if a cache
- * writer met a position outside the cache or the tables; JL_ERR_CUDA if the
- * synchronisation itself failed. */
+ * writer met a position outside the cache or the tables, or a call on a 4-bit
+ * cache a length or a page index outside it; JL_ERR_CUDA if the synchronisation
+ * itself failed. */
 jl_status jl_sync_status(jl_stream_t stream);
 
 /*
@@ -389,6 +390,105 @@ jl_status jl_decode_append_paged(const void* q, const void* k, const void* v, co
                                  const float* sin_tab, int64_t n_tab_rows, void* q_out, void* k_pool, void* v_pool,
                                  const int32_t* block_table, int32_t max_pages, int32_t page_size,
                                  int32_t num_pages, jl_stream_t stream);
+
+/*
+ * The base-RoPE KV cache held in 4 bits (the paper has no counterpart: the cache of
+ * Methodology section 2 at 9/32 of its bf16 size for head_dim 128, 5/16 for 64; the
+ * bifocal decode reads it without expanding it).
+ *
+ * Three tensors hold what k_cache and v_cache hold in bf16, contiguous or paged alike:
+ *   k_codes, v_codes  uint8 [B][cache_stride][Hkv][head_dim / 2], two codes to a byte
+ *   scales            bf16  [B][cache_stride][Hkv][8], four of the key, four of the value
+ * (paged: [num_pages][page_size] in place of [B][cache_stride]).  A row stands for
+ * x = scale * (code - 8), code in 1 .. 15.  Key scale w belongs to the rotate-half pairs
+ * (c, c + head_dim/2) with c / (head_dim/8) = w, value scale w to the channels with
+ * c / (head_dim/4) = w.  The codes' order in a row (jl_q4.cuh in csrc) is the one
+ * the decode's matrix instructions take:
+ *   key pair c, with r = c % (head_dim/8), t = r / (head_dim/32), e = r % (head_dim/32):
+ *     byte 16 t + 4 w + e (head_dim 128) or 8 t + 4 (w / 2) + 2 e + w % 2 (64); channel
+ *     c in its low four bits, c + head_dim/2 in its high four
+ *   value channel c: byte (head_dim/16) (c % 8) + c / 16, low four bits if c % 16 < 8
+ * Writing: keys are rotated as by jl_kv_cache_fill (fp32, every product and sum rounded),
+ * then scale = bf16(max |x| * fp32(1/7)) over the group and code = round(x / scale), halves to
+ * even, clamped to +-7, plus 8.  A scale below 2^-100 is stored as 0 with codes 8; a group
+ * that holds a NaN or an infinity gets a NaN scale and reads back as NaN.  The error of a
+ * value is at most half a scale (and 2^-9 of the group's largest).
+ *
+ * jl_kv_cache_fill_q4, jl_decode_append_q4: the arguments and the error behaviour of
+ * jl_kv_cache_fill and jl_decode_append, with the three tensors for the two caches; a row
+ * that is written is written whole, no other row is touched.
+ *
+ * jl_kv_cache_read_q4: rows [starts[b], lens[b]) of every entry back to bf16,
+ *   k_out[b][p - starts[b]] and v_out[b][p - starts[b]], bf16 [B][out_rows][Hkv][head_dim]
+ * (one rounding of the exact product), base-RoPE keys as jl_bifocal_prefill_chunk and
+ * jl_bifocal_decode take them.  starts: device int32 [B], NULL means 0; lens: device int32
+ * [B].  Needs 0 <= starts[b], lens[b] <= cache_stride and lens[b] - starts[b] <= out_rows;
+ * an entry outside that, and a page index outside the pool, are skipped and reported by
+ * jl_sync_status() as JL_ERR_INVALID.  Output rows behind lens[b] - starts[b] are left as
+ * they were.
+ *
+ * All tensors must be 16-byte aligned.
+ */
+jl_status jl_kv_cache_fill_q4(const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* past_lens,
+                              int32_t batch, int64_t total_tokens, int32_t Hkv, int32_t head_dim,
+                              const float* cos_tab, const float* sin_tab, int64_t n_tab_rows, void* k_codes,
+                              void* v_codes, void* scales, int64_t cache_stride, jl_stream_t stream);
+jl_status jl_kv_cache_fill_q4_paged(const void* k, const void* v, const int32_t* cu_seqlens,
+                                    const int32_t* past_lens, int32_t batch, int64_t total_tokens, int32_t Hkv,
+                                    int32_t head_dim, const float* cos_tab, const float* sin_tab, int64_t n_tab_rows,
+                                    void* k_codes, void* v_codes, void* scales, const int32_t* block_table,
+                                    int32_t max_pages, int32_t page_size, int32_t num_pages, jl_stream_t stream);
+jl_status jl_decode_append_q4(const void* q, const void* k, const void* v, const int32_t* seqlens, int32_t B,
+                              int32_t Hq, int32_t Hkv, int32_t head_dim, const float* cos_tab, const float* sin_tab,
+                              int64_t n_tab_rows, void* q_out, void* k_codes, void* v_codes, void* scales,
+                              int64_t cache_stride, jl_stream_t stream);
+jl_status jl_decode_append_q4_paged(const void* q, const void* k, const void* v, const int32_t* seqlens, int32_t B,
+                                    int32_t Hq, int32_t Hkv, int32_t head_dim, const float* cos_tab,
+                                    const float* sin_tab, int64_t n_tab_rows, void* q_out, void* k_codes,
+                                    void* v_codes, void* scales, const int32_t* block_table, int32_t max_pages,
+                                    int32_t page_size, int32_t num_pages, jl_stream_t stream);
+jl_status jl_kv_cache_read_q4(const void* k_codes, const void* v_codes, const void* scales, int64_t cache_stride,
+                              const int32_t* starts, const int32_t* lens, int32_t B, int32_t Hkv, int32_t head_dim,
+                              void* k_out, void* v_out, int64_t out_rows, jl_stream_t stream);
+jl_status jl_kv_cache_read_q4_paged(const void* k_codes, const void* v_codes, const void* scales,
+                                    const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                                    int32_t num_pages, const int32_t* starts, const int32_t* lens, int32_t B,
+                                    int32_t Hkv, int32_t head_dim, void* k_out, void* v_out, int64_t out_rows,
+                                    jl_stream_t stream);
+
+/*
+ * jl_bifocal_decode against a 4-bit cache: the same function of q, the lengths and the keys
+ * and values that the rows stand for, with the codes and scales expanded in registers.
+ * Arguments as for jl_bifocal_decode, and
+ *   seqlens      device int32 [B], 0 <= seqlens[b] <= max_seqlen; an entry of length 0 (a
+ *                padded slot of a batch) gives out = 0 and lse = -inf.  A length outside
+ *                gives NaN and is reported by jl_sync_status() as JL_ERR_INVALID.
+ *   max_seqlen   bounds the lengths; the keys are shared out by the lengths on the device,
+ *                so a large bound costs nothing and one captured call serves every step
+ *   workspace    at least jl_bifocal_decode_q4_workspace_size(Hq, head_dim) bytes, 16-byte
+ *                aligned, whatever the batch and the lengths; its contents on entry do not
+ *                matter; calls that share it must not overlap
+ * Cache rows behind an entry's length may hold anything, NaN scales too.  Paged: page_size
+ * is a multiple of 32; keys in a page outside [0, num_pages) are left out and reported by
+ * jl_sync_status() as JL_ERR_INVALID.  Supported: head_dim 64 or 128, 1 to 16 query heads
+ * per KV head, B <= 65535.
+ */
+jl_status jl_bifocal_decode_q4(const void* q, const void* k_codes, const void* v_codes, const void* scales,
+                               const int32_t* seqlens, int32_t B, int64_t cache_stride, int32_t max_seqlen,
+                               int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t w0, int32_t w_pretrained,
+                               const float* cos_tab, const float* sin_tab, int64_t n_tab_rows, float softmax_scale,
+                               void* out, float* lse, void* workspace, size_t workspace_bytes, jl_stream_t stream);
+jl_status jl_bifocal_decode_q4_paged(const void* q, const void* k_codes, const void* v_codes, const void* scales,
+                                     const int32_t* block_table, const int32_t* seqlens, int32_t B, int32_t max_pages,
+                                     int32_t page_size, int32_t num_pages, int32_t max_seqlen, int32_t Hq,
+                                     int32_t Hkv, int32_t head_dim, int32_t w0, int32_t w_pretrained,
+                                     const float* cos_tab, const float* sin_tab, int64_t n_tab_rows,
+                                     float softmax_scale, void* out, float* lse, void* workspace,
+                                     size_t workspace_bytes, jl_stream_t stream);
+
+/* Bytes of workspace jl_bifocal_decode_q4 needs: two partials per CTA, whatever the batch.
+ * 0 for non-positive sizes. */
+size_t jl_bifocal_decode_q4_workspace_size(int32_t Hq, int32_t head_dim);
 
 /*
  * jl_bifocal_decode without a caller workspace.  The paper has no counterpart:

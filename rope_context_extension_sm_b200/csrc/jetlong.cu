@@ -19,8 +19,10 @@
 #include "jetlong.h"
 #include "jl_append.cuh"
 #include "jl_decode.cuh"
+#include "jl_decode_q4.cuh"
 #include "jl_decode_tc.cuh"
 #include "jl_prefill.cuh"
+#include "jl_q4.cuh"
 #include "jl_tables.cuh"
 
 namespace {
@@ -580,6 +582,207 @@ jl_status append_common(const void* q, const void* k, const void* v, const int32
   return ok();
 }
 
+// ------------------------------------------------------------- 4-bit caches --
+
+enum class Q4Op { kFill, kAppend, kRead };
+
+// Checks shared by the 4-bit writers and the reader, then the launch.  rows: token rows
+// of a fill, entries of an append, out_rows of a read.
+jl_status q4_common(Q4Op op, jl::Q4Params& prm, int64_t rows, int32_t head_dim, bool paged, cudaStream_t st) {
+  if (prm.batch < 0 || rows < 0 || prm.Hkv < 1 || (op == Q4Op::kAppend && prm.Hq < 1))
+    return fail(JL_ERR_INVALID, "need batch >= 0, rows >= 0 and heads >= 1");
+  if (head_dim != 64 && head_dim != 128)
+    return fail(JL_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", head_dim);
+  if (paged) {
+    if (prm.page_size < 1 || prm.max_pages < 1 || prm.num_pages < 1)
+      return fail(JL_ERR_INVALID, "page_size, max_pages and num_pages must be >= 1");
+    prm.cache_stride = static_cast<int64_t>(prm.max_pages) * prm.page_size;
+  }
+  if (prm.cache_stride < 1) return fail(JL_ERR_INVALID, "cache_stride must be >= 1");
+  if (op != Q4Op::kRead && prm.n_tab_rows < 1) return fail(JL_ERR_INVALID, "n_tab_rows must be >= 1");
+  if (prm.batch == 0 || rows == 0) return ok();
+  if (!prm.lens || !prm.k_codes || !prm.v_codes || !prm.scales || (paged && !prm.block_table))
+    return fail(JL_ERR_INVALID, "null pointer argument");
+  if (op == Q4Op::kRead ? (!prm.k_out || !prm.v_out) : (!prm.k || !prm.v || !prm.cos_tab || !prm.sin_tab))
+    return fail(JL_ERR_INVALID, "null pointer argument");
+  if (op == Q4Op::kAppend && (!prm.q || !prm.q_out)) return fail(JL_ERR_INVALID, "null pointer argument");
+  const void* const all[] = {prm.k_codes, prm.v_codes, prm.scales, prm.q, prm.k, prm.v, prm.q_out, prm.k_out,
+                             prm.v_out, prm.cos_tab, prm.sin_tab};
+  for (const void* x : all)
+    if (!aligned16(x)) return fail(JL_ERR_INVALID, "every tensor must be 16-byte aligned");
+  const int64_t per = op == Q4Op::kFill ? prm.Hkv : op == Q4Op::kAppend ? prm.Hq + prm.Hkv : prm.Hkv;
+  const int64_t n = op == Q4Op::kRead ? prm.batch * rows : rows;
+  if (n > 0x7fffffffLL || n * per > 8 * 0x7fffffffLL)
+    return fail(JL_ERR_UNSUPPORTED, "too many rows for one call (%lld)", (long long)n);
+  const unsigned blocks = static_cast<unsigned>((n * per + 7) / 8);
+  const bool wide = head_dim == 128;
+  if (op == Q4Op::kFill) {
+    if (wide) jl::jl_kv_fill_q4_kernel<128><<<blocks, 256, 0, st>>>(prm);
+    else jl::jl_kv_fill_q4_kernel<64><<<blocks, 256, 0, st>>>(prm);
+  } else if (op == Q4Op::kAppend) {
+    if (wide) jl::jl_decode_append_q4_kernel<128><<<blocks, 256, 0, st>>>(prm);
+    else jl::jl_decode_append_q4_kernel<64><<<blocks, 256, 0, st>>>(prm);
+  } else {
+    if (wide) jl::jl_kv_read_q4_kernel<128><<<blocks, 256, 0, st>>>(prm);
+    else jl::jl_kv_read_q4_kernel<64><<<blocks, 256, 0, st>>>(prm);
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit cache launch");
+  return ok();
+}
+
+jl::Q4Params q4_cache(const void* k_codes, const void* v_codes, const void* scales, int64_t cache_stride,
+                      const int32_t* block_table, int32_t max_pages, int32_t page_size, int32_t num_pages) {
+  jl::Q4Params prm{};
+  prm.k_codes = static_cast<uint8_t*>(const_cast<void*>(k_codes));
+  prm.v_codes = static_cast<uint8_t*>(const_cast<void*>(v_codes));
+  prm.scales = static_cast<__nv_bfloat16*>(const_cast<void*>(scales));
+  prm.cache_stride = cache_stride;
+  prm.block_table = block_table;
+  prm.max_pages = max_pages;
+  prm.page_size = page_size;
+  prm.num_pages = num_pages;
+  return prm;
+}
+
+jl_status q4_fill(jl::Q4Params prm, const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* past_lens,
+                  int32_t batch, int64_t total_tokens, int32_t Hkv, int32_t head_dim, const float* cos_tab,
+                  const float* sin_tab, int64_t n_tab_rows, bool paged, cudaStream_t st) {
+  prm.k = static_cast<const __nv_bfloat16*>(k);
+  prm.v = static_cast<const __nv_bfloat16*>(v);
+  prm.lens = cu_seqlens;
+  prm.past = past_lens;
+  prm.batch = batch;
+  prm.total_tokens = total_tokens;
+  prm.Hkv = Hkv;
+  prm.cos_tab = cos_tab;
+  prm.sin_tab = sin_tab;
+  prm.n_tab_rows = n_tab_rows;
+  return q4_common(Q4Op::kFill, prm, total_tokens, head_dim, paged, st);
+}
+
+jl_status q4_append(jl::Q4Params prm, const void* q, const void* k, const void* v, const int32_t* seqlens, int32_t B,
+                    int32_t Hq, int32_t Hkv, int32_t head_dim, const float* cos_tab, const float* sin_tab,
+                    int64_t n_tab_rows, void* q_out, bool paged, cudaStream_t st) {
+  prm.q = static_cast<const __nv_bfloat16*>(q);
+  prm.k = static_cast<const __nv_bfloat16*>(k);
+  prm.v = static_cast<const __nv_bfloat16*>(v);
+  prm.q_out = static_cast<__nv_bfloat16*>(q_out);
+  prm.lens = seqlens;
+  prm.batch = B;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.cos_tab = cos_tab;
+  prm.sin_tab = sin_tab;
+  prm.n_tab_rows = n_tab_rows;
+  return q4_common(Q4Op::kAppend, prm, B, head_dim, paged, st);
+}
+
+jl_status q4_read(jl::Q4Params prm, const int32_t* starts, const int32_t* lens, int32_t B, int32_t Hkv,
+                  int32_t head_dim, void* k_out, void* v_out, int64_t out_rows, bool paged, cudaStream_t st) {
+  prm.past = starts;
+  prm.lens = lens;
+  prm.batch = B;
+  prm.Hkv = Hkv;
+  prm.k_out = static_cast<__nv_bfloat16*>(k_out);
+  prm.v_out = static_cast<__nv_bfloat16*>(v_out);
+  prm.out_rows = out_rows;
+  return q4_common(Q4Op::kRead, prm, out_rows, head_dim, paged, st);
+}
+
+// The decode's CTAs: one per SM.
+constexpr int32_t kDecodeQ4Ctas = 148;
+
+size_t decode_q4_ws_bytes(int32_t Hq, int32_t head_dim) {
+  if (Hq < 1 || head_dim < 1) return 0;
+  return static_cast<size_t>(kDecodeQ4Ctas) * 2 * Hq * (head_dim + 2) * sizeof(float);
+}
+
+template <int D>
+jl_status launch_decode_q4(const jl::DecodeQ4Params& prm, cudaStream_t st) {
+  cudaError_t e = launch_pdl(jl::jl_decode_q4_kernel<D>, dim3(prm.n_cta), dim3(jl::kDecodeQ4Threads), 0, st, prm);
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit decode launch");
+  e = launch_pdl(jl::jl_decode_q4_combine_kernel<D>, dim3(prm.Hq, prm.B), dim3(jl::kCombineQ4Threads), 0, st, prm);
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit decode combine launch");
+  return ok();
+}
+
+jl_status decode_q4(jl::DecodeQ4Params prm, int32_t head_dim, float softmax_scale, void* workspace,
+                    size_t workspace_bytes, bool paged, cudaStream_t st) {
+  if (prm.B < 0) return fail(JL_ERR_INVALID, "B must be >= 0 (got %d)", prm.B);
+  if (head_dim != 64 && head_dim != 128)
+    return fail(JL_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", head_dim);
+  if (prm.Hq < 1 || prm.Hkv < 1 || prm.Hq % prm.Hkv != 0)
+    return fail(JL_ERR_INVALID, "need Hq >= 1, Hkv >= 1 and Hq %% Hkv == 0 (got Hq=%d, Hkv=%d)", prm.Hq, prm.Hkv);
+  prm.group = prm.Hq / prm.Hkv;
+  if (prm.group > kMaxDecodeGroup)
+    return fail(JL_ERR_UNSUPPORTED, "decode supports 1 to %d query heads per KV head (got %d)", kMaxDecodeGroup,
+                prm.group);
+  if (prm.w0 < 0) return fail(JL_ERR_INVALID, "w0 must be >= 0 (got %d)", prm.w0);
+  if (prm.w_pre < 1) return fail(JL_ERR_INVALID, "w_pretrained must be >= 1 (got %d)", prm.w_pre);
+  if (paged) {
+    if (prm.page_size < 32 || prm.page_size % 32 != 0)
+      return fail(JL_ERR_UNSUPPORTED, "page_size must be a positive multiple of 32 (got %d)", prm.page_size);
+    if (prm.max_pages < 1 || static_cast<int64_t>(prm.max_pages) * prm.page_size < prm.max_seqlen)
+      return fail(JL_ERR_INVALID, "max_pages * page_size must cover max_seqlen");
+    if (prm.num_pages < 1 || static_cast<int64_t>(prm.num_pages) * prm.page_size > 0x7fffffffLL)
+      return fail(JL_ERR_INVALID, "num_pages * page_size must be in [1, 2^31)");
+    prm.cache_stride = static_cast<int64_t>(prm.max_pages) * prm.page_size;
+  }
+  if (prm.B == 0) return ok();
+  if (prm.max_seqlen < 1) return fail(JL_ERR_INVALID, "max_seqlen must be >= 1 (got %d)", prm.max_seqlen);
+  if (prm.cache_stride < prm.max_seqlen)
+    return fail(JL_ERR_INVALID, "cache_stride (%lld) must be >= max_seqlen (%d)", (long long)prm.cache_stride,
+                prm.max_seqlen);
+  if (prm.n_tab_rows < prm.max_seqlen)
+    return fail(JL_ERR_INVALID, "n_tab_rows (%lld) must be >= max_seqlen (%d)", (long long)prm.n_tab_rows,
+                prm.max_seqlen);
+  if (!paged && prm.B * prm.cache_stride > 0x7fffffffLL)
+    return fail(JL_ERR_UNSUPPORTED, "B * cache_stride must be < 2^31 (got %lld)", (long long)(prm.B * prm.cache_stride));
+  if (prm.B > 65535) return fail(JL_ERR_UNSUPPORTED, "B must be <= 65535 (got %d)", prm.B);
+  if (!prm.q || !prm.k_codes || !prm.v_codes || !prm.scales || !prm.seqlens || !prm.cos_tab || !prm.sin_tab ||
+      !prm.out || !workspace || (paged && !prm.block_table))
+    return fail(JL_ERR_INVALID, "null pointer argument");
+  if (!aligned16(prm.q) || !aligned16(prm.k_codes) || !aligned16(prm.v_codes) || !aligned16(prm.scales) ||
+      !aligned16(prm.out) || !aligned16(workspace) || !aligned16(prm.cos_tab) || !aligned16(prm.sin_tab))
+    return fail(JL_ERR_INVALID, "q, the cache, out, workspace and the tables must be 16-byte aligned");
+  const size_t need = decode_q4_ws_bytes(prm.Hq, head_dim);
+  if (workspace_bytes < need)
+    return fail(JL_ERR_INVALID, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
+  prm.ws = static_cast<float*>(workspace);
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
+  prm.scale_log2 = scale * 1.4426950408889634f;
+  prm.heads_per_block = 1;
+  prm.tile = 32;
+  const int64_t tiles = (static_cast<int64_t>(prm.max_seqlen) + prm.tile - 1) / prm.tile * prm.B * prm.Hkv;
+  prm.n_cta = static_cast<int32_t>(std::min<int64_t>(kDecodeQ4Ctas, tiles));
+  return head_dim == 128 ? launch_decode_q4<128>(prm, st) : launch_decode_q4<64>(prm, st);
+}
+
+jl::DecodeQ4Params decode_q4_params(const void* q, const void* k_codes, const void* v_codes, const void* scales,
+                                    const int32_t* seqlens, int32_t B, int32_t max_seqlen, int32_t Hq, int32_t Hkv,
+                                    int32_t w0, int32_t w_pretrained, const float* cos_tab, const float* sin_tab,
+                                    int64_t n_tab_rows, void* out, float* lse) {
+  jl::DecodeQ4Params prm{};
+  prm.q = static_cast<const __nv_bfloat16*>(q);
+  prm.k_codes = static_cast<const uint8_t*>(k_codes);
+  prm.v_codes = static_cast<const uint8_t*>(v_codes);
+  prm.scales = static_cast<const __nv_bfloat16*>(scales);
+  prm.seqlens = seqlens;
+  prm.B = B;
+  prm.max_seqlen = max_seqlen;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.w0 = w0;
+  prm.w_pre = w_pretrained;
+  prm.cos_tab = cos_tab;
+  prm.sin_tab = sin_tab;
+  prm.n_tab_rows = n_tab_rows;
+  prm.out = static_cast<__nv_bfloat16*>(out);
+  prm.lse = lse;
+  return prm;
+}
+
 }  // namespace
 
 // ===================================================================== ABI ==
@@ -616,7 +819,7 @@ jl_status jl_sync_status(jl_stream_t stream) {
     if (e != cudaSuccess) return cuda_fail(e, "clearing the device status word");
     if (word & jl::kDevErrTimeout) return fail(JL_ERR_TIMEOUT, "a bounded in-kernel wait ran out");
     if (word & jl::kDevErrBounds)
-      return fail(JL_ERR_INVALID, "a cache writer met a position outside the cache or the RoPE tables");
+      return fail(JL_ERR_INVALID, "a position, a length or a page index was outside the cache or the RoPE tables");
     if (word & jl::kDevErrIndex)
       return fail(JL_ERR_INVALID, "a debug-bounds check failed: a kernel derived an index outside its buffer");
   }
@@ -935,6 +1138,90 @@ jl_status jl_plain_decode(const void* q, const void* k_cache, const void* v_cach
   return decode_common(q, k_cache, v_cache, seqlens, B, cache_stride, max_seqlen, Hq, Hkv, head_dim, 0, 1, 1,
                        cos_tab, sin_tab, n_tab_rows, softmax_scale, out, lse, workspace, workspace_bytes,
                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+jl_status jl_kv_cache_fill_q4(const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* past_lens,
+                              int32_t batch, int64_t total_tokens, int32_t Hkv, int32_t head_dim,
+                              const float* cos_tab, const float* sin_tab, int64_t n_tab_rows, void* k_codes,
+                              void* v_codes, void* scales, int64_t cache_stride, jl_stream_t stream) {
+  return q4_fill(q4_cache(k_codes, v_codes, scales, cache_stride, nullptr, 0, 0, 0), k, v, cu_seqlens, past_lens,
+                 batch, total_tokens, Hkv, head_dim, cos_tab, sin_tab, n_tab_rows, false,
+                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+jl_status jl_kv_cache_fill_q4_paged(const void* k, const void* v, const int32_t* cu_seqlens,
+                                    const int32_t* past_lens, int32_t batch, int64_t total_tokens, int32_t Hkv,
+                                    int32_t head_dim, const float* cos_tab, const float* sin_tab, int64_t n_tab_rows,
+                                    void* k_codes, void* v_codes, void* scales, const int32_t* block_table,
+                                    int32_t max_pages, int32_t page_size, int32_t num_pages, jl_stream_t stream) {
+  return q4_fill(q4_cache(k_codes, v_codes, scales, 0, block_table, max_pages, page_size, num_pages), k, v,
+                 cu_seqlens, past_lens, batch, total_tokens, Hkv, head_dim, cos_tab, sin_tab, n_tab_rows, true,
+                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+jl_status jl_decode_append_q4(const void* q, const void* k, const void* v, const int32_t* seqlens, int32_t B,
+                              int32_t Hq, int32_t Hkv, int32_t head_dim, const float* cos_tab, const float* sin_tab,
+                              int64_t n_tab_rows, void* q_out, void* k_codes, void* v_codes, void* scales,
+                              int64_t cache_stride, jl_stream_t stream) {
+  return q4_append(q4_cache(k_codes, v_codes, scales, cache_stride, nullptr, 0, 0, 0), q, k, v, seqlens, B, Hq, Hkv,
+                   head_dim, cos_tab, sin_tab, n_tab_rows, q_out, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+jl_status jl_decode_append_q4_paged(const void* q, const void* k, const void* v, const int32_t* seqlens, int32_t B,
+                                    int32_t Hq, int32_t Hkv, int32_t head_dim, const float* cos_tab,
+                                    const float* sin_tab, int64_t n_tab_rows, void* q_out, void* k_codes,
+                                    void* v_codes, void* scales, const int32_t* block_table, int32_t max_pages,
+                                    int32_t page_size, int32_t num_pages, jl_stream_t stream) {
+  return q4_append(q4_cache(k_codes, v_codes, scales, 0, block_table, max_pages, page_size, num_pages), q, k, v,
+                   seqlens, B, Hq, Hkv, head_dim, cos_tab, sin_tab, n_tab_rows, q_out, true,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+jl_status jl_kv_cache_read_q4(const void* k_codes, const void* v_codes, const void* scales, int64_t cache_stride,
+                              const int32_t* starts, const int32_t* lens, int32_t B, int32_t Hkv, int32_t head_dim,
+                              void* k_out, void* v_out, int64_t out_rows, jl_stream_t stream) {
+  return q4_read(q4_cache(k_codes, v_codes, scales, cache_stride, nullptr, 0, 0, 0), starts, lens, B, Hkv, head_dim,
+                 k_out, v_out, out_rows, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+jl_status jl_kv_cache_read_q4_paged(const void* k_codes, const void* v_codes, const void* scales,
+                                    const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                                    int32_t num_pages, const int32_t* starts, const int32_t* lens, int32_t B,
+                                    int32_t Hkv, int32_t head_dim, void* k_out, void* v_out, int64_t out_rows,
+                                    jl_stream_t stream) {
+  return q4_read(q4_cache(k_codes, v_codes, scales, 0, block_table, max_pages, page_size, num_pages), starts, lens,
+                 B, Hkv, head_dim, k_out, v_out, out_rows, true, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t jl_bifocal_decode_q4_workspace_size(int32_t Hq, int32_t head_dim) { return decode_q4_ws_bytes(Hq, head_dim); }
+
+jl_status jl_bifocal_decode_q4(const void* q, const void* k_codes, const void* v_codes, const void* scales,
+                               const int32_t* seqlens, int32_t B, int64_t cache_stride, int32_t max_seqlen,
+                               int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t w0, int32_t w_pretrained,
+                               const float* cos_tab, const float* sin_tab, int64_t n_tab_rows, float softmax_scale,
+                               void* out, float* lse, void* workspace, size_t workspace_bytes, jl_stream_t stream) {
+  jl::DecodeQ4Params prm = decode_q4_params(q, k_codes, v_codes, scales, seqlens, B, max_seqlen, Hq, Hkv, w0,
+                                            w_pretrained, cos_tab, sin_tab, n_tab_rows, out, lse);
+  prm.cache_stride = cache_stride;
+  return decode_q4(prm, head_dim, softmax_scale, workspace, workspace_bytes, false,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+jl_status jl_bifocal_decode_q4_paged(const void* q, const void* k_codes, const void* v_codes, const void* scales,
+                                     const int32_t* block_table, const int32_t* seqlens, int32_t B, int32_t max_pages,
+                                     int32_t page_size, int32_t num_pages, int32_t max_seqlen, int32_t Hq,
+                                     int32_t Hkv, int32_t head_dim, int32_t w0, int32_t w_pretrained,
+                                     const float* cos_tab, const float* sin_tab, int64_t n_tab_rows,
+                                     float softmax_scale, void* out, float* lse, void* workspace,
+                                     size_t workspace_bytes, jl_stream_t stream) {
+  jl::DecodeQ4Params prm = decode_q4_params(q, k_codes, v_codes, scales, seqlens, B, max_seqlen, Hq, Hkv, w0,
+                                            w_pretrained, cos_tab, sin_tab, n_tab_rows, out, lse);
+  prm.block_table = block_table;
+  prm.max_pages = max_pages;
+  prm.page_size = page_size;
+  prm.num_pages = num_pages;
+  return decode_q4(prm, head_dim, softmax_scale, workspace, workspace_bytes, true,
+                   reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -10,6 +10,7 @@ rope_context_extension_sm_b200.build``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -73,6 +74,23 @@ SIGNATURES = {
                                         _i64, _vp]),
     "jl_decode_append": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _vp,
                                         _i64, _vp]),
+    "jl_kv_cache_fill_q4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _vp,
+                                           _i64, _vp]),
+    "jl_kv_cache_fill_q4_paged": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _i64, _vp, _vp,
+                                                 _vp, _vp, _i32, _i32, _i32, _vp]),
+    "jl_decode_append_q4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _vp,
+                                           _vp, _i64, _vp]),
+    "jl_decode_append_q4_paged": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _vp,
+                                                 _vp, _vp, _vp, _i32, _i32, _i32, _vp]),
+    "jl_kv_cache_read_q4": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _i64, _vp]),
+    "jl_kv_cache_read_q4_paged": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _vp,
+                                                 _vp, _i64, _vp]),
+    "jl_bifocal_decode_q4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _i32, _i32, _i32,
+                                            _vp, _vp, _i64, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "jl_bifocal_decode_q4_paged": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                                  _i32, _i32, _i32, _i32, _vp, _vp, _i64, _f32, _vp, _vp, _vp, _sz,
+                                                  _vp]),
+    "jl_bifocal_decode_q4_workspace_size": (_sz, [_i32, _i32]),
 }
 
 for _name, (_res, _args) in SIGNATURES.items():
@@ -433,6 +451,232 @@ def jl_decode_append_paged(q, k, v, seqlens, cos, sin, k_pool, v_pool, block_tab
                                        _ptr(block_table), block_table.shape[1], k_pool.shape[1], k_pool.shape[0],
                                        _stream(stream)), "jl_decode_append_paged")
     return q_out
+
+
+# ------------------------------------------------------------- 4-bit caches --
+
+
+def jl_kv_cache_q4_empty(n: int, stride: int, n_kv_heads: int, head_dim: int, *, device="cuda"):
+    """The three tensors (k_codes, v_codes, scales) of a 4-bit cache: [n][stride] positions,
+    or with n pages of `stride` positions a paged pool."""
+    codes = torch.empty((2, n, stride, n_kv_heads, head_dim // 2), dtype=torch.uint8, device=device)
+    return codes[0], codes[1], torch.empty((n, stride, n_kv_heads, 8), dtype=torch.bfloat16, device=device)
+
+
+def _q4_cache(k_codes, v_codes, scales, block_table=None):
+    """Checks the three tensors (and a block table); returns (Hkv, head_dim)."""
+    _need(k_codes, torch.uint8, "k_codes", 4)
+    _need(v_codes, torch.uint8, "v_codes", 4)
+    _need(scales, torch.bfloat16, "scales", 4)
+    if v_codes.shape != k_codes.shape or scales.shape != (*k_codes.shape[:3], 8):
+        raise ValueError("k_codes and v_codes must be [B][stride][Hkv][d/2] and scales [B][stride][Hkv][8]")
+    if block_table is not None:
+        _need(block_table, torch.int32, "block_table", 2)
+    return k_codes.shape[2], 2 * k_codes.shape[3]
+
+
+def _q4_shape(t: torch.Tensor, name: str, shape: tuple, dtype=torch.bfloat16) -> None:
+    _need(t, dtype, name, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+
+
+def _q4_tables(cos, sin, d: int) -> None:
+    _need(cos, torch.float32, "cos", 2)
+    _need(sin, torch.float32, "sin", 2)
+    if cos.shape != sin.shape or cos.shape[1] != d // 2:
+        raise ValueError("cos and sin must both be [n_pos][head_dim/2]")
+
+
+def _q4_alloc(stream, device):
+    """Context in which outputs and workspaces are allocated: the stream that the call runs on, so
+    that the allocator does not hand their memory to another stream's work meanwhile."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _q4_call(name: str, stream, tensors, *args) -> None:
+    """Calls the entry point on the tensors' device (all on one) and that device's current
+    stream unless one is given."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: the tensors are on different devices ({dev} and {t.device})")
+    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+        raise ValueError(f"{name}: the stream belongs to {stream.device}, the tensors are on {dev}")
+    with torch.cuda.device(dev):
+        _check(getattr(_lib, name)(*args, _stream(stream)), name)
+
+
+def _fill_q4(name, k, v, cu_seqlens, cos, sin, k_codes, v_codes, scales, past_lens, stream, block_table):
+    hkv, d = _q4_cache(k_codes, v_codes, scales, block_table)
+    T, batch = k.shape[0], cu_seqlens.shape[0] - 1
+    _q4_shape(k, "k", (T, hkv, d))
+    _q4_shape(v, "v", (T, hkv, d))
+    _q4_tables(cos, sin, d)
+    _need(cu_seqlens, torch.int32, "cu_seqlens", 1)
+    if past_lens is not None:
+        _q4_shape(past_lens, "past_lens", (batch,), torch.int32)
+    if block_table is None and k_codes.shape[0] != batch or block_table is not None and block_table.shape[0] != batch:
+        raise ValueError(f"the cache or the block table must have one entry for each of the {batch} sequences")
+    where = (k_codes.shape[1],) if block_table is None else (_ptr(block_table), block_table.shape[1], k_codes.shape[1],
+                                                             k_codes.shape[0])
+    _q4_call(name, stream, (k, v, cu_seqlens, past_lens, cos, sin, k_codes, v_codes, scales, block_table),
+             _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(past_lens), batch, T, hkv, d, _ptr(cos), _ptr(sin),
+             cos.shape[0], _ptr(k_codes), _ptr(v_codes), _ptr(scales), *where)
+    return k_codes, v_codes, scales
+
+
+def jl_kv_cache_fill_q4(k, v, cu_seqlens, cos, sin, k_codes, v_codes, scales, *, past_lens=None, stream=None):
+    """jl_kv_cache_fill into a 4-bit cache: R(p) k and v of every token, quantised as they are
+    written.  Returns the cache's three tensors."""
+    return _fill_q4("jl_kv_cache_fill_q4", k, v, cu_seqlens, cos, sin, k_codes, v_codes, scales, past_lens, stream,
+                    None)
+
+
+def jl_kv_cache_fill_q4_paged(k, v, cu_seqlens, cos, sin, k_codes, v_codes, scales, block_table, *, past_lens=None,
+                              stream=None):
+    """jl_kv_cache_fill_q4 into paged pools [num_pages][page_size][Hkv][..] through a block table."""
+    return _fill_q4("jl_kv_cache_fill_q4_paged", k, v, cu_seqlens, cos, sin, k_codes, v_codes, scales, past_lens,
+                    stream, block_table)
+
+
+def _append_q4(name, q, k, v, seqlens, cos, sin, k_codes, v_codes, scales, q_out, stream, block_table):
+    hkv, d = _q4_cache(k_codes, v_codes, scales, block_table)
+    _need(q, torch.bfloat16, "q", 3)
+    B, hq = q.shape[:2]
+    _q4_shape(q, "q", (B, hq, d))
+    _q4_shape(k, "k", (B, hkv, d))
+    _q4_shape(v, "v", (B, hkv, d))
+    _q4_shape(seqlens, "seqlens", (B,), torch.int32)
+    _q4_tables(cos, sin, d)
+    if q_out is None:
+        with _q4_alloc(stream, q.device):
+            q_out = torch.empty_like(q)
+    _q4_shape(q_out, "q_out", (B, hq, d))
+    if block_table is None and k_codes.shape[0] != B or block_table is not None and block_table.shape[0] != B:
+        raise ValueError(f"the cache or the block table must have one entry for each of the {B} tokens")
+    where = (k_codes.shape[1],) if block_table is None else (_ptr(block_table), block_table.shape[1], k_codes.shape[1],
+                                                             k_codes.shape[0])
+    _q4_call(name, stream, (q, k, v, seqlens, cos, sin, q_out, k_codes, v_codes, scales, block_table),
+             _ptr(q), _ptr(k), _ptr(v), _ptr(seqlens), B, hq, hkv, d, _ptr(cos), _ptr(sin), cos.shape[0],
+             _ptr(q_out), _ptr(k_codes), _ptr(v_codes), _ptr(scales), *where)
+    return q_out
+
+
+def jl_decode_append_q4(q, k, v, seqlens, cos, sin, k_codes, v_codes, scales, *, q_out=None, stream=None):
+    """jl_decode_append into a 4-bit cache: returns q~ = R(seqlens-1) q, quantises k~ and v of the
+    one new token per entry into the cache."""
+    return _append_q4("jl_decode_append_q4", q, k, v, seqlens, cos, sin, k_codes, v_codes, scales, q_out, stream, None)
+
+
+def jl_decode_append_q4_paged(q, k, v, seqlens, cos, sin, k_codes, v_codes, scales, block_table, *, q_out=None,
+                              stream=None):
+    """jl_decode_append_q4 into paged pools through a block table; returns q~."""
+    return _append_q4("jl_decode_append_q4_paged", q, k, v, seqlens, cos, sin, k_codes, v_codes, scales, q_out, stream,
+                      block_table)
+
+
+def _read_q4(name, k_codes, v_codes, scales, lens, starts, k_out, v_out, rows, stream, block_table):
+    hkv, d = _q4_cache(k_codes, v_codes, scales, block_table)
+    _need(lens, torch.int32, "lens", 1)
+    B = lens.shape[0]
+    if starts is not None:
+        _q4_shape(starts, "starts", (B,), torch.int32)
+    if block_table is None and k_codes.shape[0] != B or block_table is not None and block_table.shape[0] != B:
+        raise ValueError(f"the cache or the block table must have one entry for each of the {B} lengths")
+    if rows is None:
+        given = k_out if k_out is not None else v_out
+        stride = k_codes.shape[1] * (1 if block_table is None else block_table.shape[1])
+        rows = given.shape[1] if given is not None else stride
+    with _q4_alloc(stream, k_codes.device):
+        if k_out is None:
+            k_out = torch.empty((B, rows, hkv, d), dtype=torch.bfloat16, device=k_codes.device)
+        if v_out is None:
+            v_out = torch.empty((B, rows, hkv, d), dtype=torch.bfloat16, device=k_codes.device)
+    _q4_shape(k_out, "k_out", (B, rows, hkv, d))
+    _q4_shape(v_out, "v_out", (B, rows, hkv, d))
+    where = (k_codes.shape[1],) if block_table is None else (_ptr(block_table), block_table.shape[1], k_codes.shape[1],
+                                                             k_codes.shape[0])
+    _q4_call(name, stream, (k_codes, v_codes, scales, lens, starts, k_out, v_out, block_table),
+             _ptr(k_codes), _ptr(v_codes), _ptr(scales), *where, _ptr(starts), _ptr(lens), B, hkv, d, _ptr(k_out),
+             _ptr(v_out), rows)
+    return k_out, v_out
+
+
+def jl_kv_cache_read_q4(k_codes, v_codes, scales, lens, *, starts=None, k_out=None, v_out=None, rows=None,
+                        stream=None):
+    """Rows [starts[b], lens[b]) of a 4-bit cache back to bf16, at the start of k_out[b] and v_out[b]
+    ([B][rows][Hkv][d], allocated unless given; rows defaults to the cache's stride).  With starts
+    None the result is a base-RoPE cache as jl_bifocal_prefill_chunk takes it.  Returns (k, v)."""
+    return _read_q4("jl_kv_cache_read_q4", k_codes, v_codes, scales, lens, starts, k_out, v_out, rows, stream, None)
+
+
+def jl_kv_cache_read_q4_paged(k_codes, v_codes, scales, block_table, lens, *, starts=None, k_out=None, v_out=None,
+                              rows=None, stream=None):
+    """jl_kv_cache_read_q4 from paged pools through a block table."""
+    return _read_q4("jl_kv_cache_read_q4_paged", k_codes, v_codes, scales, lens, starts, k_out, v_out, rows, stream,
+                    block_table)
+
+
+def jl_bifocal_decode_q4_workspace_size(Hq: int, head_dim: int) -> int:
+    return int(_lib.jl_bifocal_decode_q4_workspace_size(Hq, head_dim))
+
+
+def _decode_q4(name, q, k_codes, v_codes, scales, seqlens, max_seqlen, w0, w_pretrained, cos, sin, softmax_scale, out,
+               lse, workspace, want_lse, stream, block_table):
+    hkv, d = _q4_cache(k_codes, v_codes, scales, block_table)
+    _need(q, torch.bfloat16, "q", 3)
+    B, hq = q.shape[:2]
+    _q4_shape(q, "q", (B, hq, d))
+    _q4_shape(seqlens, "seqlens", (B,), torch.int32)
+    _q4_tables(cos, sin, d)
+    if block_table is None and k_codes.shape[0] != B or block_table is not None and block_table.shape[0] != B:
+        raise ValueError(f"the cache or the block table must have one entry for each of the {B} queries")
+    with _q4_alloc(stream, q.device):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty((B, hq), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(jl_bifocal_decode_q4_workspace_size(hq, d), dtype=torch.uint8, device=q.device)
+    _q4_shape(out, "out", (B, hq, d))
+    if lse is not None:
+        _q4_shape(lse, "lse", (B, hq), torch.float32)
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if block_table is None:
+        where = (_ptr(seqlens), B, k_codes.shape[1])
+    else:
+        where = (_ptr(block_table), _ptr(seqlens), B, block_table.shape[1], k_codes.shape[1], k_codes.shape[0])
+    _q4_call(name, stream, (q, k_codes, v_codes, scales, seqlens, cos, sin, out, lse, workspace, block_table),
+             _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(scales), *where, max_seqlen, hq, hkv, d, w0, w_pretrained,
+             _ptr(cos), _ptr(sin), cos.shape[0], softmax_scale, _ptr(out), _ptr(lse), _ptr(workspace),
+             workspace.numel() * workspace.element_size())
+    return out, lse
+
+
+def jl_bifocal_decode_q4(q, k_codes, v_codes, scales, seqlens, max_seqlen: int, w0: int, w_pretrained: int, cos, sin,
+                         *, softmax_scale: float = 0.0, out=None, lse=None, workspace=None, want_lse: bool = True,
+                         stream=None):
+    """Single-query bifocal decode on a 4-bit base-RoPE cache (the cache is only read).
+
+    q [B][Hq][d] already rotated by R(seqlens[b]-1); the cache's tensors [B][stride][Hkv][..].
+    Entries of length 0 give out 0 and lse -inf.  Returns (out bf16 [B][Hq][d], lse fp32 [B][Hq]
+    or None)."""
+    return _decode_q4("jl_bifocal_decode_q4", q, k_codes, v_codes, scales, seqlens, max_seqlen, w0, w_pretrained, cos,
+                      sin, softmax_scale, out, lse, workspace, want_lse, stream, None)
+
+
+def jl_bifocal_decode_q4_paged(q, k_codes, v_codes, scales, block_table, seqlens, max_seqlen: int, w0: int,
+                               w_pretrained: int, cos, sin, *, softmax_scale: float = 0.0, out=None, lse=None,
+                               workspace=None, want_lse: bool = True, stream=None):
+    """jl_bifocal_decode_q4 over paged pools [num_pages][page_size][Hkv][..], block_table [B][max_pages]."""
+    return _decode_q4("jl_bifocal_decode_q4_paged", q, k_codes, v_codes, scales, seqlens, max_seqlen, w0, w_pretrained,
+                      cos, sin, softmax_scale, out, lse, workspace, want_lse, stream, block_table)
 
 
 def jl_bifocal_decode_noalloc_scratch_bytes() -> int:
