@@ -690,21 +690,65 @@ jl_status q4_read(jl::Q4Params prm, const int32_t* starts, const int32_t* lens, 
   return q4_common(Q4Op::kRead, prm, out_rows, head_dim, paged, st);
 }
 
-// The decode's CTAs: one per SM.
-constexpr int32_t kDecodeQ4Ctas = 148;
-
 size_t decode_q4_ws_bytes(int32_t Hq, int32_t head_dim) {
   if (Hq < 1 || head_dim < 1) return 0;
-  return static_cast<size_t>(kDecodeQ4Ctas) * 2 * Hq * (head_dim + 2) * sizeof(float);
+  return static_cast<size_t>(jl::kDecodeQ4Ctas) * 2 * Hq * (head_dim + 2) * sizeof(float);
 }
 
-template <int D>
+// [rows][heads][bytes] tensor, box = one row's bytes x 32 rows x `box_heads` heads, which
+// lands as [head][row][bytes].
+jl_status make_q4_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int bytes, int box_heads) {
+  auto fn = encode_fn();
+  if (!fn) return fail(JL_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(bytes), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads) * bytes, static_cast<cuuint64_t>(bytes)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(bytes), 32, static_cast<cuuint32_t>(box_heads)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(JL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return JL_OK;
+}
+
+template <int D, int NQ, int HPW>
 jl_status launch_decode_q4(const jl::DecodeQ4Params& prm, cudaStream_t st) {
-  cudaError_t e = launch_pdl(jl::jl_decode_q4_kernel<D>, dim3(prm.n_cta), dim3(jl::kDecodeQ4Threads), 0, st, prm);
+  const int64_t rows = prm.block_table != nullptr ? static_cast<int64_t>(prm.num_pages) * prm.page_size
+                                                  : prm.B * prm.cache_stride;
+  CUtensorMap tk, tv, ts;
+  jl_status s;
+  if ((s = make_q4_map(&tk, prm.k_codes, rows, prm.Hkv, D / 2, prm.heads_per_block)) != JL_OK) return s;
+  if ((s = make_q4_map(&tv, prm.v_codes, rows, prm.Hkv, D / 2, prm.heads_per_block)) != JL_OK) return s;
+  if ((s = make_q4_map(&ts, prm.scales, rows, prm.Hkv, 16, prm.heads_per_block)) != JL_OK) return s;
+  const int smem = jl::decode_q4_layout(D, NQ, HPW, prm.heads_per_block, prm.tile).total;
+  auto kern = jl::jl_decode_q4_kernel<D, NQ, HPW>;
+  const KernelAttr attr = kernel_attr(reinterpret_cast<const void*>(kern), 222 * 1024);
+  if (attr.err != cudaSuccess) return cuda_fail(attr.err, "cudaFuncSetAttribute(4-bit decode)");
+  if (attr.regs < jl::kDecodeQ4Regs)  // setmaxnreg draws on the launch's registers and would wait for good
+    return fail(JL_ERR_UNSUPPORTED, "4-bit decode built with %d registers per thread; the register split needs %d",
+                attr.regs, jl::kDecodeQ4Regs);
+  cudaError_t e = launch_pdl(kern, dim3(prm.n_cta), dim3(jl::kDecodeQ4Threads), smem, st, tk, tv, ts, prm);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit decode launch");
   e = launch_pdl(jl::jl_decode_q4_combine_kernel<D>, dim3(prm.Hq, prm.B), dim3(jl::kCombineQ4Threads), 0, st, prm);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit decode combine launch");
   return ok();
+}
+
+template <int D>
+jl_status dispatch_decode_q4(jl::DecodeQ4Params& prm, cudaStream_t st) {
+  // Score tiles of four query heads; KV heads of a block (they share the cos/sin rows and fill
+  // the eight key warps); keys of a tile: sixteen for each warp of a head.
+  const int nq = prm.group <= 4 ? 1 : prm.group <= 8 ? 2 : 4;
+  int hpb = 8 / nq;
+  while (prm.Hkv % hpb != 0) hpb /= 2;
+  const int hpw = nq == 1 && hpb >= 2 ? 2 : 1;
+  prm.heads_per_block = hpb;
+  prm.tile = std::max(32, 16 * jl::kDecodeQ4KeyWarps * hpw / hpb);
+  const int64_t tiles = (static_cast<int64_t>(prm.max_seqlen) + prm.tile - 1) / prm.tile * prm.B * (prm.Hkv / hpb);
+  prm.n_cta = static_cast<int32_t>(std::min<int64_t>(jl::kDecodeQ4Ctas, tiles));
+  if (nq == 4) return launch_decode_q4<D, 4, 1>(prm, st);
+  if (nq == 2) return launch_decode_q4<D, 2, 1>(prm, st);
+  return hpw == 2 ? launch_decode_q4<D, 1, 2>(prm, st) : launch_decode_q4<D, 1, 1>(prm, st);
 }
 
 jl_status decode_q4(jl::DecodeQ4Params prm, int32_t head_dim, float softmax_scale, void* workspace,
@@ -752,11 +796,7 @@ jl_status decode_q4(jl::DecodeQ4Params prm, int32_t head_dim, float softmax_scal
   prm.ws = static_cast<float*>(workspace);
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
   prm.scale_log2 = scale * 1.4426950408889634f;
-  prm.heads_per_block = 1;
-  prm.tile = 32;
-  const int64_t tiles = (static_cast<int64_t>(prm.max_seqlen) + prm.tile - 1) / prm.tile * prm.B * prm.Hkv;
-  prm.n_cta = static_cast<int32_t>(std::min<int64_t>(kDecodeQ4Ctas, tiles));
-  return head_dim == 128 ? launch_decode_q4<128>(prm, st) : launch_decode_q4<64>(prm, st);
+  return head_dim == 128 ? dispatch_decode_q4<128>(prm, st) : dispatch_decode_q4<64>(prm, st);
 }
 
 jl::DecodeQ4Params decode_q4_params(const void* q, const void* k_codes, const void* v_codes, const void* scales,
