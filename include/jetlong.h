@@ -469,7 +469,7 @@ jl_status jl_kv_cache_read_q4_paged(const void* k_codes, const void* v_codes, co
  *                aligned, whatever the batch and the lengths; its contents on entry do not
  *                matter; calls that share it must not overlap
  * Cache rows behind an entry's length may hold anything, NaN scales too.  Paged: page_size
- * is a multiple of 32; a page outside [0, num_pages) is read as zeros and reported by
+ * is a multiple of 16; a page outside [0, num_pages) is read as zeros and reported by
  * jl_sync_status() as JL_ERR_INVALID.  Supported: head_dim 64 or 128, 1 to 16 query heads
  * per KV head, B <= 65535.
  */

@@ -695,60 +695,69 @@ size_t decode_q4_ws_bytes(int32_t Hq, int32_t head_dim) {
   return static_cast<size_t>(jl::kDecodeQ4Ctas) * 2 * Hq * (head_dim + 2) * sizeof(float);
 }
 
-// [rows][heads][bytes] tensor, box = one row's bytes x 32 rows x `box_heads` heads, which
-// lands as [head][row][bytes].
-jl_status make_q4_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int bytes, int box_heads) {
+// [rows][groups][width bytes] tensor, box = `width` bytes x 16 rows x `box` groups, which lands
+// as [group][row][width], swizzled by its width.
+jl_status make_q4_map(CUtensorMap* map, const void* base, int64_t rows, int groups, int width, int box_groups) {
   auto fn = encode_fn();
   if (!fn) return fail(JL_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(bytes), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads) * bytes, static_cast<cuuint64_t>(bytes)};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(bytes), 32, static_cast<cuuint32_t>(box_heads)};
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(groups)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(groups) * width, static_cast<cuuint64_t>(width)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(width), 16, static_cast<cuuint32_t>(box_groups)};
   cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapSwizzle swizzle = width == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : width == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                                   : CU_TENSOR_MAP_SWIZZLE_NONE;
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(JL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
   return JL_OK;
 }
 
-template <int D, int NQ, int HPW>
+template <int D, int NQ, int KEYS>
 jl_status launch_decode_q4(const jl::DecodeQ4Params& prm, cudaStream_t st) {
   const int64_t rows = prm.block_table != nullptr ? static_cast<int64_t>(prm.num_pages) * prm.page_size
                                                   : prm.B * prm.cache_stride;
   CUtensorMap tk, tv, ts;
   jl_status s;
-  if ((s = make_q4_map(&tk, prm.k_codes, rows, prm.Hkv, D / 2, prm.heads_per_block)) != JL_OK) return s;
-  if ((s = make_q4_map(&tv, prm.v_codes, rows, prm.Hkv, D / 2, prm.heads_per_block)) != JL_OK) return s;
-  if ((s = make_q4_map(&ts, prm.scales, rows, prm.Hkv, 16, prm.heads_per_block)) != JL_OK) return s;
-  const int smem = jl::decode_q4_layout(D, NQ, HPW, prm.heads_per_block, prm.tile).total;
-  auto kern = jl::jl_decode_q4_kernel<D, NQ, HPW>;
+  const int hpb = prm.heads_per_block, width = jl::q4_code_row(D, hpb), groups = prm.Hkv * (D / 2) / width;
+  if ((s = make_q4_map(&tk, prm.k_codes, rows, groups, width, hpb * (D / 2) / width)) != JL_OK) return s;
+  if ((s = make_q4_map(&tv, prm.v_codes, rows, groups, width, hpb * (D / 2) / width)) != JL_OK) return s;
+  if ((s = make_q4_map(&ts, prm.scales, rows, prm.Hkv / hpb, 16 * hpb, 1)) != JL_OK) return s;
+  const int smem = jl::decode_q4_layout(D, NQ, KEYS, prm.heads_per_block, prm.tile).total;
+  auto kern = jl::jl_decode_q4_kernel<D, NQ, KEYS>;
   const KernelAttr attr = kernel_attr(reinterpret_cast<const void*>(kern), 222 * 1024);
   if (attr.err != cudaSuccess) return cuda_fail(attr.err, "cudaFuncSetAttribute(4-bit decode)");
-  if (attr.regs < jl::kDecodeQ4Regs)  // setmaxnreg draws on the launch's registers and would wait for good
+  if (attr.regs < jl::DecodeQ4Warps<KEYS>::kRegs)  // setmaxnreg draws on the launch's registers and would wait for good
     return fail(JL_ERR_UNSUPPORTED, "4-bit decode built with %d registers per thread; the register split needs %d",
-                attr.regs, jl::kDecodeQ4Regs);
-  cudaError_t e = launch_pdl(kern, dim3(prm.n_cta), dim3(jl::kDecodeQ4Threads), smem, st, tk, tv, ts, prm);
+                attr.regs, jl::DecodeQ4Warps<KEYS>::kRegs);
+  cudaError_t e = launch_pdl(kern, dim3(prm.n_cta), dim3(jl::DecodeQ4Warps<KEYS>::kThreads), smem, st, tk, tv, ts, prm);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit decode launch");
-  e = launch_pdl(jl::jl_decode_q4_combine_kernel<D>, dim3(prm.Hq, prm.B), dim3(jl::kCombineQ4Threads), 0, st, prm);
+  // Four blocks a head while that leaves room on the SMs (148 of four or more blocks each).
+  const bool split = static_cast<int64_t>(prm.Hq) * prm.B * 4 <= 1024;
+  e = launch_pdl(split ? jl::jl_decode_q4_combine_kernel<D, 4> : jl::jl_decode_q4_combine_kernel<D, 1>,
+                 dim3(prm.Hq * (split ? 4 : 1), prm.B), dim3(jl::kCombineQ4Threads), 0, st, prm);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit decode combine launch");
   return ok();
 }
 
 template <int D>
 jl_status dispatch_decode_q4(jl::DecodeQ4Params& prm, cudaStream_t st) {
-  // Score tiles of four query heads; KV heads of a block (they share the cos/sin rows and fill
-  // the eight key warps); keys of a tile: sixteen for each warp of a head.
+  // Score tiles of four query heads; KV heads of a block (they share the cos/sin rows); key
+  // warps; keys of a tile: sixteen for each warp of a head, Q4_NB times.
   const int nq = prm.group <= 4 ? 1 : prm.group <= 8 ? 2 : 4;
   int hpb = 8 / nq;
   while (prm.Hkv % hpb != 0) hpb /= 2;
-  const int hpw = nq == 1 && hpb >= 2 ? 2 : 1;
+  const int keys = 8;
   prm.heads_per_block = hpb;
-  prm.tile = std::max(32, 16 * jl::kDecodeQ4KeyWarps * hpw / hpb);
+  prm.tile = (nq == 1 ? 16 * Q4_U : 16) * keys / hpb;
   const int64_t tiles = (static_cast<int64_t>(prm.max_seqlen) + prm.tile - 1) / prm.tile * prm.B * (prm.Hkv / hpb);
+  if (tiles > 0x7fffffff) return fail(JL_ERR_UNSUPPORTED, "too many keys for one call (%lld tiles)", (long long)tiles);
   prm.n_cta = static_cast<int32_t>(std::min<int64_t>(jl::kDecodeQ4Ctas, tiles));
-  if (nq == 4) return launch_decode_q4<D, 4, 1>(prm, st);
-  if (nq == 2) return launch_decode_q4<D, 2, 1>(prm, st);
-  return hpw == 2 ? launch_decode_q4<D, 1, 2>(prm, st) : launch_decode_q4<D, 1, 1>(prm, st);
+  if (nq == 4) return launch_decode_q4<D, 4, 8>(prm, st);
+  if (nq == 2) return launch_decode_q4<D, 2, 8>(prm, st);
+  return launch_decode_q4<D, 1, 8>(prm, st);
 }
 
 jl_status decode_q4(jl::DecodeQ4Params prm, int32_t head_dim, float softmax_scale, void* workspace,
@@ -765,8 +774,8 @@ jl_status decode_q4(jl::DecodeQ4Params prm, int32_t head_dim, float softmax_scal
   if (prm.w0 < 0) return fail(JL_ERR_INVALID, "w0 must be >= 0 (got %d)", prm.w0);
   if (prm.w_pre < 1) return fail(JL_ERR_INVALID, "w_pretrained must be >= 1 (got %d)", prm.w_pre);
   if (paged) {
-    if (prm.page_size < 32 || prm.page_size % 32 != 0)
-      return fail(JL_ERR_UNSUPPORTED, "page_size must be a positive multiple of 32 (got %d)", prm.page_size);
+    if (prm.page_size < 16 || prm.page_size % 16 != 0)  // sixteen keys of a box lie in one page
+      return fail(JL_ERR_UNSUPPORTED, "page_size must be a positive multiple of 16 (got %d)", prm.page_size);
     if (prm.max_pages < 1 || static_cast<int64_t>(prm.max_pages) * prm.page_size < prm.max_seqlen)
       return fail(JL_ERR_INVALID, "max_pages * page_size must cover max_seqlen");
     if (prm.num_pages < 1 || static_cast<int64_t>(prm.num_pages) * prm.page_size > 0x7fffffffLL)

@@ -52,10 +52,12 @@ __device__ __forceinline__ int q4_tiles(const DecodeQ4Params& p, int L) {
   return L < 1 || L > p.max_seqlen ? 0 : (L + p.tile - 1) / p.tile;
 }
 
-// Tiles of all entries, and of the entries before b, by one warp.
-__device__ __forceinline__ int2 q4_tiles_before(const DecodeQ4Params& p, int b, int lane) {
-  int all = 0, before = 0;
-  for (int e = lane; e < p.B; e += 32) {
+// Tiles of all entries, and of the entries before b, by one warp; `first` is the tiles of
+// entry `lane`.
+__device__ __forceinline__ int2 q4_tiles_before(const DecodeQ4Params& p, int b, int lane, int& first) {
+  first = lane < p.B ? q4_tiles(p, p.seqlens[lane]) : 0;
+  int all = first, before = lane < b ? first : 0;
+  for (int e = lane + 32; e < p.B; e += 32) {
     const int t = q4_tiles(p, p.seqlens[e]);
     all += t;
     before += e < b ? t : 0;
@@ -70,33 +72,35 @@ __device__ __forceinline__ int2 q4_tiles_before(const DecodeQ4Params& p, int b, 
 
 // CTAs that get a range (every one of at least a tile), the first tile of CTA c's range, and
 // the CTA that holds tile x.
-__device__ __forceinline__ int q4_ctas(const DecodeQ4Params& p, int64_t total) {
-  return static_cast<int>(min(static_cast<int64_t>(p.n_cta), total));
+__device__ __forceinline__ int q4_ctas(const DecodeQ4Params& p, int total) { return min(p.n_cta, total); }
+__device__ __forceinline__ int q4_range_begin(int total, int n_cta, int c) {  // floor(total c / n_cta)
+  const unsigned q = static_cast<unsigned>(total) / n_cta, r = static_cast<unsigned>(total) % n_cta;
+  return q * c + r * static_cast<unsigned>(c) / n_cta;
 }
-__device__ __forceinline__ int64_t q4_range_begin(int64_t total, int n_cta, int c) { return total * c / n_cta; }
-__device__ __forceinline__ int q4_cta_of(int64_t total, int n_cta, int64_t x) {
-  return static_cast<int>(((x + 1) * n_cta - 1) / total);
+__device__ __forceinline__ int q4_cta_of(int total, int n_cta, int x) {
+  return static_cast<int>(((x + 1LL) * n_cta - 1) / total);
 }
 
 // Where a range starts: entry and tile inside it.
 struct Q4Start {
   int hb, b, tile;
-  int64_t begin, end;  // the range in the list of all tiles
+  int begin, end;  // the range in the list of all tiles (the host keeps their number below 2^31)
 };
 
 __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
   Q4Start s{0, 0, 0, 0, 0};
-  const int all = q4_tiles_before(p, 0, lane).x;
-  const int64_t total = static_cast<int64_t>(all) * (p.Hkv / p.heads_per_block);
+  int t;
+  const int all = q4_tiles_before(p, 0, lane, t).x;
+  const int total = all * (p.Hkv / p.heads_per_block);
   const int n_cta = q4_ctas(p, total);
   if (static_cast<int>(blockIdx.x) >= n_cta) return s;
   s.begin = q4_range_begin(total, n_cta, blockIdx.x);
   s.end = q4_range_begin(total, n_cta, blockIdx.x + 1);
-  s.hb = static_cast<int>(s.begin / all);
-  int left = static_cast<int>(s.begin % all);
+  s.hb = s.begin / all;
+  int left = s.begin % all;
   for (int e0 = 0; e0 < p.B; e0 += 32) {
     const int e = e0 + lane;
-    const int t = e < p.B ? q4_tiles(p, p.seqlens[e]) : 0;
+    if (e0 > 0) t = e < p.B ? q4_tiles(p, p.seqlens[e]) : 0;
     int sum = t;  // inclusive prefix over the lanes
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -117,9 +121,9 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 
 // ------------------------------------------------------------- the decode kernel --
 //
-// Shape.  12 warps a CTA: eight take keys (below), four prepare what they need.  A tile is
-// `tile` keys of all KV heads of a head block; it arrives by TMA as [head][32 keys][row]
-// boxes of key codes, value codes and scales, in a ring of stages.
+// Shape.  Eight or sixteen warps of a CTA take keys, four prepare what they need.  A tile is
+// `tile` keys of all KV heads of a head block: sixteen keys for each key warp, of one or two
+// heads.  It arrives by TMA as boxes of sixteen keys, in a ring of stages.
 //
 // Matrix instructions: mma.m16n8k16 with the keys on M for the scores and the channels on M
 // for the values.  A lane expands the codes of its own fragment in registers: four to six
@@ -148,15 +152,21 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 // for the whole head block: from the table's row of the tile's first key by steps of one
 // position in fp32 (at most 32 steps), stored as fp16 in the order of the fragments.
 
+#ifndef Q4_U
+#define Q4_U 2
+#endif
 constexpr int kDecodeQ4Ctas = 148;  // one per SM
-constexpr int kDecodeQ4KeyWarps = 8, kDecodeQ4TabWarps = 4;
-constexpr int kDecodeQ4Threads = 32 * (kDecodeQ4KeyWarps + kDecodeQ4TabWarps);
+constexpr int kDecodeQ4TabWarps = 3, kDecodeQ4OtherWarps = 1 + kDecodeQ4TabWarps;  // one loads
 constexpr int kDecodeQ4MaxStages = 6;
-// Registers a thread: 168 at launch; the key warps rise to 216, the others drop to 72.
-constexpr int kDecodeQ4Regs = 168, kDecodeQ4KeyRegs = 216, kDecodeQ4TabRegs = 72;
-static_assert(kDecodeQ4KeyWarps * kDecodeQ4KeyRegs + kDecodeQ4TabWarps * kDecodeQ4TabRegs <=
-                  (kDecodeQ4KeyWarps + kDecodeQ4TabWarps) * kDecodeQ4Regs,
-              "the split has to fit the launch's registers, or setmaxnreg waits for good");
+
+// Key warps of a CTA, and the registers a thread at launch, of the key warps and of the others.
+template <int KW>
+struct DecodeQ4Warps {
+  static constexpr int kThreads = 32 * (KW + kDecodeQ4OtherWarps);
+  static constexpr int kRegs = KW == 8 ? 168 : 96, kKeyRegs = KW == 8 ? 216 : 104, kTabRegs = KW == 8 ? 72 : 64;
+  static_assert(KW * kKeyRegs + kDecodeQ4OtherWarps * kTabRegs <= (KW + kDecodeQ4OtherWarps) * kRegs,
+                "the split has to fit the launch's registers, or setmaxnreg waits for good");
+};
 
 // Shared memory: a region for the query fragments, reused to join the key warps, then the
 // stages.  A stage: key codes, value codes, scales, cos/sin rows.
@@ -164,11 +174,11 @@ struct DecodeQ4Layout {
   int region, codes, scales, table, stage, stages, total;
 };
 
-// NQ: score tiles of four query heads; HPB: KV heads of a block; HPW: of a key warp.
-__host__ __device__ constexpr DecodeQ4Layout decode_q4_layout(int D, int NQ, int HPW, int HPB, int tile) {
+// NQ: score tiles of four query heads; KW: key warps; HPB: KV heads of a block.
+__host__ __device__ constexpr DecodeQ4Layout decode_q4_layout(int D, int NQ, int KW, int HPB, int tile) {
   DecodeQ4Layout l{};
-  const int frags = 2 * HPB * NQ * (D / 32) * 512, join = kDecodeQ4KeyWarps * HPW * NQ * 4 * D * 4;
-  l.region = frags > join ? frags : join;
+  const int frags = 2 * HPB * NQ * (D / 32) * 512, join = KW * NQ * 4 * (D + 8) * 4;
+  l.region = ((frags > join ? frags : join) + 1023) / 1024 * 1024;
   l.codes = tile * HPB * D / 2;
   l.scales = tile * HPB * 16;
   l.table = tile * D * 2;
@@ -180,11 +190,10 @@ __host__ __device__ constexpr DecodeQ4Layout decode_q4_layout(int D, int NQ, int
 }
 
 struct DecodeQ4Shared {
-  uint64_t full[kDecodeQ4MaxStages];   // codes and scales have arrived
-  uint64_t turned[kDecodeQ4MaxStages]; // cos/sin rows are written
+  uint64_t full[kDecodeQ4MaxStages];   // codes and scales have arrived, cos/sin rows are written
   uint64_t empty[kDecodeQ4MaxStages];
   float mul[32];                       // log2 units per unit of score, by query head of the block
-  float red_m[kDecodeQ4KeyWarps][16], red_l[kDecodeQ4KeyWarps][16];
+  float red_m[16][16], red_l[16][16];
   Q4Start start;
   int abort;
 };
@@ -194,13 +203,20 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same with a zero accumulator.
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+template <int KW>
 __device__ __forceinline__ void key_warps_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kDecodeQ4KeyWarps) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * KW) : "memory");
 }
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
@@ -221,34 +237,59 @@ __device__ __forceinline__ __half2 codes_f16(uint32_t w) {
     return __hsub2(bits_h2(select_or(w, 0x000f000fu, 0x64006400u)), __float2half2_rn(1032.f));
 }
 
-// Row r of a block's sixteen keys holds key q4_key_of(r): neighbouring rows are keys of
-// opposite parity, and rows 0, 2, 4, 6 (and 1, 3, 5, 7) fall on different banks in the
-// swizzled code boxes, so both the key and the value loads are free of bank conflicts.
-__device__ __forceinline__ int q4_key_of(int r) { return r ^ ((r >> 1) & 1); }
+// Value codes are fed as they are: four bits at the bottom of an fp16 are the subnormal
+// n 2^-24, in the high four bits of its byte n 2^-20, both exact operands of the matrix
+// instruction.  The 8 that every code is over is taken off at the end, 8 times the sum of
+// the weights as the matrix instruction sums them (kEights is 8 in both units); against sums
+// of codes of 0 .. 15 that loses no more than a bit.
+constexpr uint32_t kEightsLow = 0x00080008u, kEightsHigh = 0x00800080u;
 
-// Shared-memory offset of byte x of key `key`'s codes in a [keys][D/2] box (64-byte swizzle
-// for D = 128, none for D = 64).
-template <int D>
-__device__ __forceinline__ int q4_code_at(int key, int x) {
-  return D == 128 ? key * 64 + (x ^ (((key >> 1) & 3) << 4)) : key * 32 + x;
+__device__ __forceinline__ void prefetch_l2(const void* x) { asm volatile("prefetch.global.L2 [%0];" ::"l"(x)); }
+
+// Shared-memory loads by 32-bit address, in order with the barrier waits around them.
+template <int OFF = 0>
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4+%5];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at), "n"(OFF));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Row r of a warp's sixteen keys holds key q4_key_of(r).  Neighbouring rows differ in parity
+// and in bit 2, rows 0, 2, 4, 6 (and 1, 3, 5, 7) in bits 1 and 2, so that the key, value,
+// scale and cos/sin loads are all free of bank conflicts in the swizzled boxes.
+__device__ __forceinline__ int q4_key_of(int r) { return r ^ ((r & 1) << 2); }
+
+// A box holds sixteen keys in rows of neighbouring heads, 128 bytes where the block has that
+// many (TMA takes a row at a time: rows of 64 bytes, one head each, took twice as long as the
+// arithmetic), with the swizzle of that row length.  Bytes of a row of codes, and the offset
+// of byte x of key `key`'s row of `width` bytes.
+__host__ __device__ constexpr int q4_code_row(int D, int HPB) { return HPB * D / 2 < 128 ? HPB * D / 2 : 128; }
+__device__ __forceinline__ int q4_at(int width, int key, int x) {
+  const int turn = width == 128 ? key & 7 : width == 64 ? (key >> 1) & 3 : width == 32 ? (key >> 2) & 1 : 0;
+  return key * width + (x ^ (turn << 4));
 }
 
-// Offset of 16-byte chunk (word w, lane t) of cos/sin row r.
+// Offset of 16-byte chunk (word w, lane t) of a key's cos/sin row.
 template <int D>
-__device__ __forceinline__ int q4_turn_at(int r, int w, int t) {
-  return r * 2 * D + ((w * 64 + t * 16) ^ ((r & 1) << 6));  // neighbouring rows on different banks
+__device__ __forceinline__ int q4_turn_at(int key, int w, int t) {
+  return key * 2 * D + ((w * 64 + t * 16) ^ ((key & 1) << 6));  // neighbouring rows on different banks
 }
 
-// floor(x / G) for x < G + 128: G < 128 by a 16-bit reciprocal (x < 256, exact since
-// x * G < 2^16), a larger G by one comparison.
-struct SmallDiv {
-  int g, magic;
-  __device__ __forceinline__ explicit SmallDiv(int G) : g(G), magic(G < 128 ? (65536 + G - 1) / G : 0) {}
-  __device__ __forceinline__ int operator()(int x) const { return magic ? (x * magic) >> 16 : (x >= g ? 1 : 0); }
-};
-
-template <int D, int NQ, int HPW>
-__global__ void __launch_bounds__(kDecodeQ4Threads, 1)
+template <int D, int NQ, int KEYS>
+__global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
     jl_decode_q4_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                         const __grid_constant__ CUtensorMap ts, const DecodeQ4Params p) {
   constexpr int HALF = D / 2;
@@ -256,21 +297,22 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
   constexpr int VW = D / 64;    // of its value codes
   constexpr int MT = D / 16;    // output tiles of 16 channels
   constexpr int NP = (NQ + 1) / 2;  // value tiles of eight columns
-  constexpr bool kQueryRegs = NQ * HPW <= 2;
+  constexpr int kF = NQ == 1 ? 2 : 4;  // weight fragments: pairs of scale groups, or groups
+  constexpr bool kQueryRegs = NQ <= 2;  // query fragments stay in registers
+  constexpr int U = NQ == 1 ? Q4_U : 1;    // sixteens of keys that a warp takes at once
   extern __shared__ uint8_t raw_smem[];
   __shared__ DecodeQ4Shared sh;
   uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   const int HPB = p.heads_per_block, T = p.tile;
-  const DecodeQ4Layout lay = decode_q4_layout(D, NQ, HPW, HPB, T);
+  const DecodeQ4Layout lay = decode_q4_layout(D, NQ, KEYS, HPB, T);
   uint8_t* const stages = smem + lay.region;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &sh.abort;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < lay.stages; ++s) {
-      mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.turned[s], kDecodeQ4TabWarps);
-      mbar_init(&sh.empty[s], kDecodeQ4KeyWarps);
+      mbar_init(&sh.full[s], kDecodeQ4OtherWarps);
+      mbar_init(&sh.empty[s], KEYS);
     }
     sh.abort = 0;
     fence_mbar_init();
@@ -281,97 +323,157 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
   griddep_wait();  // the cache, the lengths and the query may come from the previous kernel
   griddep_launch_dependents();
   if (warp == 0) {
+    const bool failed = status_failed();
     Q4Start s = q4_range(p, lane);
-    if (__any_sync(0xffffffffu, status_failed())) s.end = s.begin;
+    if (__any_sync(0xffffffffu, failed)) s.end = s.begin;
     if (lane == 0) sh.start = s;
+    if (s.begin < s.end) {
+      // The first segment's query and the tables' row for it are asked for before the loads of
+      // the tiles, behind which they would queue for some microseconds.
+      const char* q = reinterpret_cast<const char*>(p.q + (static_cast<int64_t>(s.b) * p.Hq + s.hb * HPB * p.group) * D);
+      for (int x = lane * 128; x < HPB * p.group * D * 2; x += 32 * 128) prefetch_l2(q + x);
+      const int i = p.seqlens[s.b] - 1, nq = i - i / max(1, (i + p.w_pre) / p.w_pre);
+      if (lane < 2 * HALF * 4 / 128)
+        prefetch_l2((lane & 1 ? p.sin_tab : p.cos_tab) + static_cast<int64_t>(nq) * HALF + (lane >> 1) * 32);
+    }
   }
   __syncthreads();
   const Q4Start st = sh.start;
-  int64_t cur = st.begin;
+  int cur = st.begin;
   int hb = st.hb, b = st.b, t0 = st.tile;
   int stage = 0;
   uint32_t phase = 0;
 
-  if (warp >= kDecodeQ4KeyWarps) {
-    // ------------------------------------------------ loads and cos/sin rows --
-    setmaxnreg_dec<kDecodeQ4TabRegs>();
-    const int tw = warp - kDecodeQ4KeyWarps;
-    const int per = T / kDecodeQ4TabWarps;  // rows of this warp
-    // lane -> the two pairs of one packed register: word w, fragment lane t, register half e
-    const bool has = D == 128 || lane < 16;
-    const int w = D == 128 ? lane / 8 : (lane & 15) / 8, t = D == 128 ? (lane / 2) & 3 : lane & 3;
-    const int e = D == 128 ? lane & 1 : (lane >> 2) & 1;
-    const int c0 = D == 128 ? 16 * w + 4 * t + e : 8 * (2 * w + e) + 2 * t, c1 = D == 128 ? c0 + 2 : c0 + 1;
-    float step_c[2] = {1.f, 1.f}, step_s[2] = {0.f, 0.f};
-    if (p.n_tab_rows > 1) {
-      step_c[0] = p.cos_tab[HALF + c0], step_s[0] = p.sin_tab[HALF + c0];
-      step_c[1] = p.cos_tab[HALF + c1], step_s[1] = p.sin_tab[HALF + c1];
-    }
-    int issued = 0;
+  if (warp >= KEYS) {
+    setmaxnreg_dec<DecodeQ4Warps<KEYS>::kTabRegs>();
     bool ok = true;
-    while (cur < st.end && ok) {
-      const int L = p.seqlens[b], tiles = q4_tiles(p, L);
-      const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (st.end - cur)));
-      const int grow = max(1, (L + p.w_pre - 1) / p.w_pre);
-      const int jb = grow > 1 ? L - 1 - p.w0 : -1;  // remote keys are j <= jb
-      int quot = (t0 * T) / grow, rem = (t0 * T) % grow;
-      const int dq = T / grow, dr = T % grow;
-      for (int tile = t0; tile < t1; ++tile) {
-        const int j0 = tile * T;
-        const bool remote = j0 <= jb;
-        float ac[2], as[2];
-        if (remote) {
-          const int64_t row = min(static_cast<int64_t>(j0 - quot + tw * per), p.n_tab_rows - 1) * HALF;
-          JL_CHECK(row >= 0 && quot == j0 / grow && j0 - quot < p.n_tab_rows);
-          ac[0] = p.cos_tab[row + c0], as[0] = p.sin_tab[row + c0];
-          ac[1] = p.cos_tab[row + c1], as[1] = p.sin_tab[row + c1];
-        }
-        if (!warp_wait(&sh.empty[stage], phase ^ 1, abort)) {
-          ok = false;
-          break;
-        }
-        uint8_t* base = stages + stage * lay.stage;
-        if (tw == 0 && lane == 0) {
-          mbar_arrive_expect_tx(&sh.full[stage], 2 * lay.codes + lay.scales);
-          for (int x = 0; x < T / 32; ++x) {
-            int row = static_cast<int>(b * p.cache_stride + j0 + 32 * x);
+    if (warp == KEYS) {
+      // ---------------------------------------------------------------- loads --
+      const int boxes = T / 16, rows = HPB * HALF / q4_code_row(D, HPB);  // of a tile; of codes, a key
+      int issued = 0;
+      while (cur < st.end && ok) {
+        const int L = p.seqlens[b], tiles = q4_tiles(p, L);
+        const int t1 = min(tiles, t0 + (st.end - cur));
+        int row = 0;  // lane x: the cache row of box x of the 32 asked for last
+        for (int tile = t0; tile < t1; ++tile) {
+          const int at = (tile - t0) * boxes % 32;
+          if (at == 0) {
+            const int j = tile * T + 16 * lane;
+            row = static_cast<int>(b * p.cache_stride + j);
             if (p.block_table != nullptr) {
               // pages behind the length need no entry: their keys are never used
-              const int j = j0 + 32 * x;
               const int page = j < L ? p.block_table[static_cast<int64_t>(b) * p.max_pages + j / p.page_size] : 0;
               const bool there = page >= 0 && page < p.num_pages;
               if (!there) atomicOr(&g_status, kDevErrBounds);
               row = (there ? page : p.num_pages) * p.page_size + (there ? j % p.page_size : 0);  // outside reads zeros
             }
-            tma_load_3d(base + x * HPB * 32 * HALF, &tk, &sh.full[stage], 0, row, hb * HPB);
-            tma_load_3d(base + lay.codes + x * HPB * 32 * HALF, &tv, &sh.full[stage], 0, row, hb * HPB);
-            tma_load_3d(base + 2 * lay.codes + x * HPB * 512, &ts, &sh.full[stage], 0, row, hb * HPB);
+          }
+          if (!warp_wait(&sh.empty[stage], phase ^ 1, abort)) {
+            ok = false;
+            break;
+          }
+          uint8_t* base = stages + stage * lay.stage;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.full[stage], 2 * lay.codes + lay.scales);
+          __syncwarp();
+          if (lane >= at && lane < at + boxes) {
+            const int x = lane - at;
+            tma_load_3d(base + x * HPB * 16 * HALF, &tk, &sh.full[stage], 0, row, hb * rows);
+            tma_load_3d(base + lay.codes + x * HPB * 16 * HALF, &tv, &sh.full[stage], 0, row, hb * rows);
+            tma_load_3d(base + 2 * lay.codes + x * HPB * 256, &ts, &sh.full[stage], 0, row, hb);
+          }
+          ++issued;
+          if (++stage == lay.stages) {
+            stage = 0;
+            phase ^= 1;
           }
         }
-        ++issued;
-        if (remote && has) {
-          uint8_t* tab = base + 2 * lay.codes + lay.scales;
-#pragma unroll 4
-          for (int r = tw * per; r < (tw + 1) * per; ++r) {
-            uint8_t* at = tab + q4_turn_at<D>(r, w, t) + 4 * e;
-            *reinterpret_cast<__half2*>(at) = __floats2half2_rn(ac[0], ac[1]);
-            *reinterpret_cast<__half2*>(at + 8) = __floats2half2_rn(as[0], as[1]);
+        cur += t1 - t0;
+        t0 = 0;
+        if (++b == p.B) {
+          b = 0;
+          ++hb;
+        }
+      }
+      if (!ok && lane == 0) {
+        // gave up: the copies in flight land before the block leaves its shared memory
+        for (int x = max(0, issued - lay.stages); x < issued; ++x)
+          mbar_wait_bounded(&sh.full[x % lay.stages], (x / lay.stages) & 1);
+      }
+      return;
+    }
+    // ------------------------------------------------------------ cos/sin rows --
+    // Eight keys at a time, the warps in turn; each eight starts from the tables' row of its
+    // first key (row j - floor(j / G)) and steps on.  That row is asked for one eight ahead,
+    // after it was brought into L2 some tiles ahead.
+    const int tw = warp - KEYS - 1;
+    // lane -> the two pairs of one packed register: word w, fragment lane t, register half e
+    const bool has = D == 128 || lane < 16;
+    const int w = D == 128 ? lane / 8 : (lane & 15) / 8, t = D == 128 ? (lane / 2) & 3 : lane & 3;
+    const int e = D == 128 ? lane & 1 : (lane >> 2) & 1;
+    const int c0 = D == 128 ? 16 * w + 4 * t + e : 8 * (2 * w + e) + 2 * t, c1 = D == 128 ? c0 + 2 : c0 + 1;
+    // one position's step of both pairs, packed; with a table of one row nothing is remote
+    const int64_t one = p.n_tab_rows > 1 ? HALF : 0;
+    const uint64_t step_c = f2_pack(p.cos_tab[one + c0], p.cos_tab[one + c1]);
+    const uint64_t step_s = f2_pack(p.sin_tab[one + c0], p.sin_tab[one + c1]);
+    const uint64_t step_n = f2_pack(-p.sin_tab[one + c0], -p.sin_tab[one + c1]);
+    while (cur < st.end && ok) {
+      const int L = p.seqlens[b], tiles = q4_tiles(p, L);
+      const int t1 = min(tiles, t0 + (st.end - cur));
+      const int grow = max(1, (L + p.w_pre - 1) / p.w_pre);
+      const int jb = grow > 1 ? L - 1 - p.w0 : -1;  // remote keys are j <= jb
+      const int far_tiles = jb < 0 ? 0 : min(t1, jb / T + 1);
+      const int ahead = 4 * T - 4 * T / grow;  // rows that four tiles on begins further, or one more
+      float2 next_c = make_float2(1.f, 1.f), next_s = make_float2(0.f, 0.f);
+      int next_left = grow;
+      auto ask = [&](int j) {  // keys behind the length may have no row
+        const int quot = j / grow;
+        next_left = grow - (j - quot * grow);  // keys until f steps; that key keeps the angle of the one before it
+        const int64_t row = min(static_cast<int64_t>(j - quot), p.n_tab_rows - 1) * HALF;
+        next_c = make_float2(p.cos_tab[row + c0], p.cos_tab[row + c1]);
+        next_s = make_float2(p.sin_tab[row + c0], p.sin_tab[row + c1]);
+        const int64_t later = min(static_cast<int64_t>(j - quot) + ahead, p.n_tab_rows - 1) * HALF;
+        prefetch_l2(p.cos_tab + later + c0);
+        prefetch_l2(p.sin_tab + later + c0);
+      };
+      if (t0 < far_tiles) ask(t0 * T + 8 * tw);
+      for (int tile = t0; tile < t1; ++tile) {
+        if (!warp_wait(&sh.empty[stage], phase ^ 1, abort)) {
+          ok = false;
+          break;
+        }
+        if (tile < far_tiles) {
+          uint8_t* const rows = stages + stage * lay.stage + 2 * lay.codes + lay.scales;
+          for (int r = 8 * tw; r < T; r += 8 * kDecodeQ4TabWarps) {
+            uint64_t ac = f2_pack(next_c.x, next_c.y), as = f2_pack(next_s.x, next_s.y);
+            int left = next_left;
+            const int r_next = r + 8 * kDecodeQ4TabWarps;
+            if (r_next < T) ask(tile * T + r_next);
+            else if (tile + 1 < far_tiles) ask((tile + 1) * T + 8 * tw);
+            // even and odd rows from two places, so that the offsets are constants
+            uint8_t* even = rows + q4_turn_at<D>(r, w, t) + 4 * e;
+            uint8_t* odd = rows + q4_turn_at<D>(r + 1, w, t) + 4 * e - 2 * D;
+            if (has) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float nc = ac[x] * step_c[x] - as[x] * step_s[x];
-              as[x] = as[x] * step_c[x] + ac[x] * step_s[x];
-              ac[x] = nc;
+              for (int x = 0; x < 8; ++x) {
+                uint8_t* at = (x & 1 ? odd : even) + x * 2 * D;
+                float c[2], sn[2];
+                f2_unpack(ac, c[0], c[1]);
+                f2_unpack(as, sn[0], sn[1]);
+                *reinterpret_cast<__half2*>(at) = __floats2half2_rn(c[0], c[1]);
+                *reinterpret_cast<__half2*>(at + 8) = __floats2half2_rn(sn[0], sn[1]);
+                if (--left == 0) {
+                  left = grow;
+                } else {
+                  const uint64_t nc = f2_fma(ac, step_c, f2_mul(as, step_n));
+                  as = f2_fma(as, step_c, f2_mul(ac, step_s));
+                  ac = nc;
+                }
+              }
             }
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.turned[stage]);
-        quot += dq;
-        rem += dr;
-        if (rem >= grow) {
-          rem -= grow;
-          ++quot;
-        }
+        if (lane == 0) mbar_arrive(&sh.full[stage]);
         if (++stage == lay.stages) {
           stage = 0;
           phase ^= 1;
@@ -384,52 +486,68 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
         ++hb;
       }
     }
-    if (!ok && tw == 0 && lane == 0) {
-      // gave up: the copies in flight land before the block leaves its shared memory
-      for (int x = max(0, issued - lay.stages); x < issued; ++x)
-        mbar_wait_bounded(&sh.full[x % lay.stages], (x / lay.stages) & 1);
-    }
     return;
   }
 
   // ------------------------------------------------------------------ the keys --
-  setmaxnreg_inc<kDecodeQ4KeyRegs>();
+  setmaxnreg_inc<DecodeQ4Warps<KEYS>::kKeyRegs>();
   const int g = lane >> 2, t = lane & 3;
-  const int wph = kDecodeQ4KeyWarps * HPW / HPB;  // warps that share a head, each its own blocks of keys
-  const int wsub = warp % wph, h0 = warp / wph * HPW;  // this warp's first KV head in the block
-  const int keyA = q4_key_of(g);                       // its rows' keys in a block: keyA, keyA + 8
-  const int key0 = q4_key_of(2 * t), key1 = q4_key_of(2 * t + 1);  // and its value rows' keys
-  uint4* const frags = reinterpret_cast<uint4*>(smem);  // [2][HPB][NQ][KW][32]
-  float* const join = reinterpret_cast<float*>(smem);   // [warps][HPW][4 NQ][D]
+  const int wph = KEYS / HPB;                          // warps that share a head
+  const int wsub = warp % wph, head = warp / wph;      // this warp's place among them, its KV head in the block
+  const int keyA = q4_key_of(g);                       // its score rows' keys of a sixteen: keyA, keyA + 8
+  const int key0 = q4_key_of(2 * t), key1 = q4_key_of(2 * t + 1);  // its value fragments': these and 8 on
+  const int width = q4_code_row(D, HPB), in_row = width / HALF;    // a row of codes and its heads
+  const uint32_t eight = 8 * width, next_codes = HPB * 16 * HALF, next_scales = HPB * 256;  // eight keys, a box on
+  // offsets in a stage
+  const int box = wsub * U * HPB * 16 * HALF + head / in_row * 16 * width, x0 = head % in_row * HALF;
+  const uint32_t at_key = box + q4_at(width, keyA, x0 + t * KW * 4);
+  const uint32_t at_val0 = lay.codes + box + q4_at(width, key0, x0 + g * MT);
+  const uint32_t at_val1 = lay.codes + box + q4_at(width, key1, x0 + g * MT);
+  const uint32_t at_scale = 2 * lay.codes + wsub * U * HPB * 256 + q4_at(HPB * 16, keyA, head * 16);
+  const uint32_t at_turn0 = 2 * lay.codes + lay.scales + q4_turn_at<D>(wsub * 16 * U + keyA, 0, t);  // words 0, 2
+  const uint32_t at_turn1 = 2 * lay.codes + lay.scales + q4_turn_at<D>(wsub * 16 * U + keyA, 1, t);  // words 1, 3
+  const uint32_t stages_at = smem_u32(stages);
+  const uint32_t frags_at = smem_u32(smem) + head * NQ * KW * 512 + lane * 16;  // [2][HPB][NQ][KW][32] uint4
+  const uint32_t far_frags = HPB * NQ * KW * 512;
+  float* const join = reinterpret_cast<float*>(smem);  // [warps][4 NQ][D + 8]: the four heads of a tile on different banks
   bool ok = true;
 
   while (cur < st.end) {
     const int L = p.seqlens[b], tiles = q4_tiles(p, L);
-    const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (st.end - cur)));
+    const int t1 = min(tiles, t0 + (st.end - cur));
     if (t1 > t0) {
       const int i = L - 1, grow = max(1, (L + p.w_pre - 1) / p.w_pre);
       const int jb = grow > 1 ? i - p.w0 : -1;
 
-      // Query fragments, a head of the block at a time: local and remote variant, each split
-      // into two fp16 columns.
+      // Query fragments: this warp's query heads of the block, local and remote variant, each
+      // split into two fp16 columns.  All loads come first.
       {
+        constexpr int kRows = 32 / KEYS;  // HPB * NQ <= 8
         const int nq = i - i / grow;
         const bool has = D == 128 || lane < 16;
         const int w = D == 128 ? lane / 8 : (lane & 15) / 8, ft = D == 128 ? (lane / 2) & 3 : lane & 3;
         const int e = D == 128 ? lane & 1 : (lane >> 2) & 1;
         const int c0 = D == 128 ? 16 * w + 4 * ft + e : 8 * (2 * w + e) + 2 * ft, c1 = D == 128 ? c0 + 2 : c0 + 1;
+        float y[kRows][4];  // channels c0, c1, c0 + D/2, c1 + D/2
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          const int x = warp + u * KEYS, h = x / (4 * NQ), qh = x % (4 * NQ);  // KV head, query head of its group
+#pragma unroll
+          for (int n = 0; n < 4; ++n) y[u][n] = 0.f;
+          if (h < HPB && qh < p.group && has) {
+            const __nv_bfloat16* qp = p.q + (static_cast<int64_t>(b) * p.Hq + (hb * HPB + h) * p.group + qh) * D;
+            y[u][0] = __bfloat162float(qp[c0]), y[u][1] = __bfloat162float(qp[c1]);
+            y[u][2] = __bfloat162float(qp[c0 + HALF]), y[u][3] = __bfloat162float(qp[c1 + HALF]);
+          }
+        }
         float cs[2], sn[2];
         cs[0] = p.cos_tab[static_cast<int64_t>(nq) * HALF + c0], cs[1] = p.cos_tab[static_cast<int64_t>(nq) * HALF + c1];
         sn[0] = p.sin_tab[static_cast<int64_t>(nq) * HALF + c0], sn[1] = p.sin_tab[static_cast<int64_t>(nq) * HALF + c1];
-        for (int x = warp; x < HPB * 4 * NQ; x += kDecodeQ4KeyWarps) {
-          const int h = x / (4 * NQ), qh = x % (4 * NQ);  // KV head of the block, query head of its group
-          float lo[2] = {0.f, 0.f}, hi[2] = {0.f, 0.f};
-          if (qh < p.group && has) {
-            const __nv_bfloat16* qp = p.q + (static_cast<int64_t>(b) * p.Hq + (hb * HPB + h) * p.group + qh) * D;
-            lo[0] = __bfloat162float(qp[c0]), lo[1] = __bfloat162float(qp[c1]);
-            hi[0] = __bfloat162float(qp[c0 + HALF]), hi[1] = __bfloat162float(qp[c1 + HALF]);
-          }
-          float top = fmaxf(fmaxf(fabsf(lo[0]), fabsf(lo[1])), fmaxf(fabsf(hi[0]), fabsf(hi[1])));
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          const int x = warp + u * KEYS, h = x / (4 * NQ), qh = x % (4 * NQ);
+          if (h >= HPB) break;
+          float top = fmaxf(fmaxf(fabsf(y[u][0]), fabsf(y[u][1])), fmaxf(fabsf(y[u][2]), fabsf(y[u][3])));
 #pragma unroll
           for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           // 2^up brings the largest channel into [8, 16); up in [-120, 120] keeps both factors normal
@@ -439,19 +557,18 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
           if (has) {
 #pragma unroll
             for (int var = 0; var < 2; ++var) {
-              float y[4];  // channels c0, c1, c0 + D/2, c1 + D/2
-#pragma unroll
-              for (int n = 0; n < 2; ++n) {
-                y[n] = (var ? lo[n] * cs[n] + hi[n] * sn[n] : lo[n]) * f;
-                y[2 + n] = (var ? hi[n] * cs[n] - lo[n] * sn[n] : hi[n]) * f;
-              }
-              uint32_t* at = reinterpret_cast<uint32_t*>(frags + (((var * HPB + h) * NQ + qh / 4) * KW + w) * 32);
+              uint32_t* at = reinterpret_cast<uint32_t*>(smem) + (((var * HPB + h) * NQ + qh / 4) * KW + w) * 128;
               const int col = 2 * (qh & 3);
 #pragma unroll
-              for (int n = 0; n < 2; ++n) {
-                const __half2 big = __floats2half2_rn(y[2 * n], y[2 * n + 1]);
+              for (int n = 0; n < 2; ++n) {  // low channels, high channels
+                float v[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+                  v[z] = (var == 0 ? y[u][2 * n + z] : n == 0 ? y[u][z] * cs[z] + y[u][2 + z] * sn[z]
+                                                              : y[u][2 + z] * cs[z] - y[u][z] * sn[z]) * f;
+                const __half2 big = __floats2half2_rn(v[0], v[1]);
                 const float2 bf = __half22float2(big);
-                const __half2 small = __floats2half2_rn(y[2 * n] - bf.x, y[2 * n + 1] - bf.y);
+                const __half2 small = __floats2half2_rn(v[0] - bf.x, v[1] - bf.y);
                 const int reg = D == 128 ? 2 * n + e : 2 * e + n;
                 at[(col * 4 + ft) * 4 + reg] = h2_bits(big);
                 at[((col + 1) * 4 + ft) * 4 + reg] = h2_bits(small);
@@ -460,102 +577,83 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
           }
         }
       }
-      key_warps_sync();
+      key_warps_sync<KEYS>();
 
-      float o[HPW][NP][MT][4], m[HPW][NQ], l[HPW][NQ], mul[HPW][NQ];
-      uint4 qf[kQueryRegs ? HPW * NQ * KW : 1];
+      float o[NP][MT][4], eights[NP][kF][4], m[NQ], l[NQ], mul[NQ];
+      uint4 qf[kQueryRegs ? NQ * KW : 1];
       int have = -1;  // the variant that qf holds
 #pragma unroll
-      for (int h = 0; h < HPW; ++h) {
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          m[h][n] = -INFINITY;
-          l[h][n] = 0.f;
-          mul[h][n] = sh.mul[(h0 + h) * 4 * NQ + 4 * n + t];
-        }
-#pragma unroll
-        for (int n = 0; n < NP; ++n)
-#pragma unroll
-          for (int x = 0; x < MT; ++x)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) o[h][n][x][y] = 0.f;
+      for (int n = 0; n < NQ; ++n) {
+        m[n] = -INFINITY;
+        l[n] = 0.f;
+        mul[n] = sh.mul[head * 4 * NQ + 4 * n + t];
       }
-      const SmallDiv div(grow);
-      int rem = (t0 * T) % grow;
-      const int dr = T % grow;
-
-      for (int tile = t0; tile < t1; ++tile) {
-        const int j0 = tile * T;
-        if (ok) ok = warp_wait(&sh.full[stage], phase, abort) && warp_wait(&sh.turned[stage], phase, abort);
-        const uint8_t* base = stages + stage * lay.stage;
-        const uint8_t* tab = base + 2 * lay.codes + lay.scales;
-        for (int blk = wsub; blk < T / 16 && ok; blk += wph) {
-          const int jblk = j0 + blk * 16;
-          if (jblk >= L) break;
-          const int x0 = (blk >> 1) * HPB * 32, first = (blk & 1) * 16;  // box, and the block's first key in it
-          const bool any_far = jblk <= jb, all_far = jblk + 15 <= jb || L - 1 <= jb, tail = jblk + 16 > L;
-          float s[HPW][NQ][2];  // scores of rows g and g + 8, head 4 n + t
-
-          uint32_t kc[HPW][2][KW];
-          float ks[HPW][2][4], vs[HPW][2][4];
 #pragma unroll
-          for (int h = 0; h < HPW; ++h)
+      for (int n = 0; n < NP; ++n)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+#pragma unroll
+          for (int x = 0; x < MT; ++x) o[n][x][y] = 0.f;
+#pragma unroll
+          for (int f = 0; f < kF; ++f) eights[n][f][y] = 0.f;
+        }
+
+      int j = t0 * T + wsub * 16 * U;  // the warp's first key of the tile
+      for (int tile = t0; tile < t1; ++tile, j += T) {
+        if (ok) ok = warp_wait(&sh.full[stage], phase, abort);
+        if (ok && j < L) {
+          const uint32_t base = stages_at + stage * lay.stage;
+          const uint32_t ka = base + at_key, sa = base + at_scale;
+          uint32_t kc[U][2][KW];
+          uint2 ks[U][2];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const int key = first + keyA + 8 * r;
-              const uint8_t* at = base + (x0 + (h0 + h) * 32) * HALF + q4_code_at<D>(key, t * KW * 4);
+              const uint32_t at = ka + u * next_codes + r * eight;
               if constexpr (D == 128) {
-                const uint4 v = *reinterpret_cast<const uint4*>(at);
-                kc[h][r][0] = v.x, kc[h][r][1] = v.y, kc[h][r][2] = v.z, kc[h][r][3] = v.w;
+                const uint4 v = lds128(at);
+                kc[u][r][0] = v.x, kc[u][r][1] = v.y, kc[u][r][2] = v.z, kc[u][r][3] = v.w;
               } else {
-                const uint2 v = *reinterpret_cast<const uint2*>(at);
-                kc[h][r][0] = v.x, kc[h][r][1] = v.y;
+                const uint2 v = lds64(at);
+                kc[u][r][0] = v.x, kc[u][r][1] = v.y;
               }
-              uint4 sc = *reinterpret_cast<const uint4*>(base + 2 * lay.codes + (x0 + (h0 + h) * 32 + key) * 16);
-              if (tail && jblk + keyA + 8 * r >= L) sc = make_uint4(0u, 0u, 0u, 0u);  // weight 0 times a NaN scale is NaN
-              ks[h][r][0] = __uint_as_float(sc.x << 16), ks[h][r][1] = __uint_as_float(sc.x & 0xffff0000u);
-              ks[h][r][2] = __uint_as_float(sc.y << 16), ks[h][r][3] = __uint_as_float(sc.y & 0xffff0000u);
-              vs[h][r][0] = __uint_as_float(sc.z << 16), vs[h][r][1] = __uint_as_float(sc.z & 0xffff0000u);
-              vs[h][r][2] = __uint_as_float(sc.w << 16), vs[h][r][3] = __uint_as_float(sc.w & 0xffff0000u);
+              ks[u][r] = lds64(sa + u * next_scales + r * 128 * HPB);
             }
-          const int d0 = blk * 16 + keyA;  // row of the tile's cos/sin rows: d - floor((rem + d) / G)
-          const int rowA = d0 - div(rem + d0), rowB = d0 + 8 - div(rem + d0 + 8);
-          JL_CHECK(rowA >= 0 && rowB < T && rem < grow && rem == j0 % grow);
 
-          // Scores of this block under one variant of the query (and, far, of the keys).
-          auto scores = [&](auto far_tag, float (&dst)[HPW][NQ][2]) {
+          // Scores under one variant of the query (and, far, of the keys); rows g and g + 8 of
+          // each sixteen, head 4 n + t.
+          float s[U][NQ][2];
+          auto scores = [&](auto far_tag, auto& dst) {
             constexpr bool FAR = decltype(far_tag)::value;
+            const uint32_t fa = frags_at + (FAR ? far_frags : 0u);
             if constexpr (kQueryRegs) {
               if (have != FAR) {
                 have = FAR;
 #pragma unroll
-                for (int h = 0; h < HPW; ++h)
-#pragma unroll
-                  for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                    for (int w = 0; w < KW; ++w)
-                      qf[(h * NQ + n) * KW + w] = frags[(((FAR * HPB + h0 + h) * NQ + n) * KW + w) * 32 + lane];
+                for (int x = 0; x < NQ * KW; ++x) qf[x] = lds128(fa + x * 512);
               }
             }
+            const uint32_t turn0 = base + at_turn0, turn1 = base + at_turn1;
 #pragma unroll
-            for (int h = 0; h < HPW; ++h)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-              for (int n = 0; n < NQ; ++n) dst[h][n][0] = dst[h][n][1] = 0.f;
+              for (int n = 0; n < NQ; ++n) dst[u][n][0] = dst[u][n][1] = 0.f;
 #pragma unroll
-            for (int w = 0; w < KW; ++w) {
-              uint4 turn[2];
-              if constexpr (FAR) {
-                turn[0] = *reinterpret_cast<const uint4*>(tab + q4_turn_at<D>(rowA, w, t));
-                turn[1] = *reinterpret_cast<const uint4*>(tab + q4_turn_at<D>(rowB, w, t));
-              }
+            for (int w = 0; w < KW; ++w)
 #pragma unroll
-              for (int h = 0; h < HPW; ++h) {
+              for (int u = 0; u < U; ++u) {
+                uint4 turn[2];
+                if constexpr (FAR) {
+                  turn[0] = lds128((w & 1 ? turn1 : turn0) + u * 32 * D + (w >> 1) * 128);
+                  turn[1] = lds128((w & 1 ? turn1 : turn0) + u * 32 * D + (w >> 1) * 128 + 16 * D);
+                }
                 uint32_t lo[2][2], hi[2][2];  // [row][register half]
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
                   for (int e = 0; e < 2; ++e) {
-                    const uint32_t word = e ? kc[h][r][w] >> 8 : kc[h][r][w];
+                    const uint32_t word = e ? kc[u][r][w] >> 8 : kc[u][r][w];
                     __half2 a = codes_f16<false>(word), bb = codes_f16<true>(word);
                     if constexpr (FAR) {  // R(-n)
                       const __half2 c = bits_h2(e ? turn[r].y : turn[r].x), sn = bits_h2(e ? turn[r].w : turn[r].z);
@@ -568,122 +666,151 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
                   }
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
-                  const uint4 q = kQueryRegs ? qf[kQueryRegs ? (h * NQ + n) * KW + w : 0]
-                                             : frags[(((FAR * HPB + h0 + h) * NQ + n) * KW + w) * 32 + lane];
+                  uint4 q;
+                  if constexpr (kQueryRegs) q = qf[n * KW + w];
+                  else q = lds128(fa + (n * KW + w) * 512);
                   if constexpr (D == 128) {  // a word is one group: two steps, low channels then high
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16(c, {lo[0][0], lo[1][0], lo[0][1], lo[1][1]}, q.x, q.y);
+                    float c[4];
+                    mma_f16_zero(c, {lo[0][0], lo[1][0], lo[0][1], lo[1][1]}, q.x, q.y);
                     mma_f16(c, {hi[0][0], hi[1][0], hi[0][1], hi[1][1]}, q.z, q.w);
-                    dst[h][n][0] = fmaf(ks[h][0][w], c[0] + c[1], dst[h][n][0]);
-                    dst[h][n][1] = fmaf(ks[h][1][w], c[2] + c[3], dst[h][n][1]);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                      const uint32_t sc = w < 2 ? ks[u][r].x : ks[u][r].y;
+                      dst[u][n][r] = fmaf(w & 1 ? bf16_high(sc) : bf16_low(sc), c[2 * r] + c[2 * r + 1], dst[u][n][r]);
+                    }
                   } else {  // two groups, a step each
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                      float c[4] = {0.f, 0.f, 0.f, 0.f};
-                      mma_f16(c, {lo[0][e], lo[1][e], hi[0][e], hi[1][e]}, e ? q.z : q.x, e ? q.w : q.y);
-                      dst[h][n][0] = fmaf(ks[h][0][2 * w + e], c[0] + c[1], dst[h][n][0]);
-                      dst[h][n][1] = fmaf(ks[h][1][2 * w + e], c[2] + c[3], dst[h][n][1]);
+                      float c[4];
+                      mma_f16_zero(c, {lo[0][e], lo[1][e], hi[0][e], hi[1][e]}, e ? q.z : q.x, e ? q.w : q.y);
+#pragma unroll
+                      for (int r = 0; r < 2; ++r) {
+                        const uint32_t sc = w == 0 ? ks[u][r].x : ks[u][r].y;
+                        dst[u][n][r] = fmaf(e ? bf16_high(sc) : bf16_low(sc), c[2 * r] + c[2 * r + 1], dst[u][n][r]);
+                      }
                     }
                   }
                 }
               }
-            }
           };
-          if (!any_far) {
-            scores(std::false_type{}, s);
-          } else if (all_far) {
-            scores(std::true_type{}, s);
-          } else {  // the block that straddles the window edge
-            float near[HPW][NQ][2];
-            scores(std::true_type{}, s);
+          if (j <= jb) scores(std::true_type{}, s);
+          if (j + 16 * U - 1 > jb) {  // local keys, and the local ones where the window edge passes
+            float near[U][NQ][2];
             scores(std::false_type{}, near);
 #pragma unroll
-            for (int h = 0; h < HPW; ++h)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
               for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) s[h][n][r] = jblk + keyA + 8 * r <= jb ? s[h][n][r] : near[h][n][r];
+                for (int r = 0; r < 2; ++r)
+                  s[u][n][r] = j + 16 * u + keyA + 8 * r <= jb ? s[u][n][r] : near[u][n][r];
           }
 
           // Weights and their products with the value scales.  M moves only when a product
-          // passes 2^14 (in the first block: by anything), so most blocks rescale nothing.
-          float wt[HPW][NQ][2];
+          // passes 2^14 (in the first keys: by anything), so it rarely does.
+          uint2 vs[U][2];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) vs[u][r] = lds64(sa + u * next_scales + r * 128 * HPB + 8);
+          if (j + 16 * U > L) {  // keys behind the length: weight 0, and no NaN scale that it could meet
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                if (j + 16 * u + keyA + 8 * r >= L) {
+                  vs[u][r] = make_uint2(0u, 0u);
+#pragma unroll
+                  for (int n = 0; n < NQ; ++n) s[u][n][r] = -INFINITY;
+                }
+            asm volatile("" ::: "memory");  // a branch: one tile of an entry takes it
+          }
+          float wt[U][NQ][2];
           bool over = false;
 #pragma unroll
-          for (int h = 0; h < HPW; ++h)
+          for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const float top = fmaxf(fmax3(vs[h][r][0], vs[h][r][1], vs[h][r][2]), fmaxf(vs[h][r][3], 0x1p-90f));
+              const uint2 v = vs[u][r];
+              const float top = fmaxf(fmax3(bf16_low(v.x), bf16_high(v.x), bf16_low(v.y)), fmaxf(bf16_high(v.y), 0x1p-90f));
 #pragma unroll
               for (int n = 0; n < NQ; ++n) {
-                s[h][n][r] *= mul[h][n];
-                if (tail && jblk + keyA + 8 * r >= L) s[h][n][r] = -INFINITY;
-                wt[h][n][r] = ex2_approx(s[h][n][r] - m[h][n]);
-                over |= wt[h][n][r] * top > 0x1p14f;
+                wt[u][n][r] = ex2_approx(fmaf(s[u][n][r], mul[n], -m[n]));
+                over |= wt[u][n][r] * top > 0x1p14f;
               }
             }
           if (__any_sync(0xffffffffu, over)) {
+            float f[NQ];
 #pragma unroll
-            for (int h = 0; h < HPW; ++h) {
-              float f[NQ];
+            for (int n = 0; n < NQ; ++n) {
+              float top = m[n] + 10.f;
 #pragma unroll
-              for (int n = 0; n < NQ; ++n) {
-                float top = m[h][n] + 10.f;
+              for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                  const float big = fmaxf(fmax3(vs[h][r][0], vs[h][r][1], vs[h][r][2]), fmaxf(vs[h][r][3], 0x1p-90f));
-                  top = fmaxf(top, s[h][n][r] + log2f(big));
+                  const uint2 v = vs[u][r];
+                  const float big = fmaxf(fmax3(bf16_low(v.x), bf16_high(v.x), bf16_low(v.y)), fmaxf(bf16_high(v.y), 0x1p-90f));
+                  top = fmaxf(top, fmaf(s[u][n][r], mul[n], __log2f(big)));
                 }
 #pragma unroll
-                for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                const float now = top - 10.f;
-                f[n] = m[h][n] == -INFINITY ? 0.f : ex2_approx(m[h][n] - now);
-                m[h][n] = now;
-                l[h][n] *= f[n];
-                wt[h][n][0] = ex2_approx(s[h][n][0] - now);
-                wt[h][n][1] = ex2_approx(s[h][n][1] - now);
-              }
+              for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+              const float now = top - 10.f;
+              f[n] = m[n] == -INFINITY ? 0.f : ex2_approx(m[n] - now);
+              m[n] = now;
+              l[n] *= f[n];
 #pragma unroll
-              for (int n = 0; n < NP; ++n)
+              for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int x = 0; x < MT; ++x)
-#pragma unroll
-                  for (int y = 0; y < 4; ++y) o[h][n][x][y] *= f[NQ == 1 ? 0 : 2 * n + (y & 1)];
+                for (int r = 0; r < 2; ++r) wt[u][n][r] = ex2_approx(fmaf(s[u][n][r], mul[n], -now));
             }
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float by = f[NQ == 1 ? 0 : 2 * n + (y & 1)];
+#pragma unroll
+                for (int x = 0; x < MT; ++x) o[n][x][y] *= by;
+#pragma unroll
+                for (int x = 0; x < kF; ++x) eights[n][x][y] *= by;
+              }
           }
 
           // Values.  Column 2t of the weights is head t of score tile 2n, column 2t + 1 of
           // tile 2n + 1; with one score tile both are head t, the even columns under the
           // scales of the even groups and the odd ones under those of the odd groups.
 #pragma unroll
-          for (int h = 0; h < HPW; ++h) {
-            constexpr int kF = NQ == 1 ? 2 : 4;  // scaled fragments: pairs of groups, or groups
+          for (int u = 0; u < U; ++u) {
             uint32_t pf[NP][kF][2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
+              const float vf[4] = {bf16_low(vs[u][r].x), bf16_high(vs[u][r].x), bf16_low(vs[u][r].y), bf16_high(vs[u][r].y)};
 #pragma unroll
-              for (int n = 0; n < NQ; ++n) l[h][n] += wt[h][n][r];
+              for (int n = 0; n < NQ; ++n) l[n] += wt[u][n][r];
 #pragma unroll
               for (int n = 0; n < NP; ++n)
 #pragma unroll
                 for (int f = 0; f < kF; ++f) {
-                  const float a = wt[h][NQ == 1 ? 0 : 2 * n][r] * vs[h][r][NQ == 1 ? 2 * f : f];
-                  const float bb = wt[h][NQ == 1 ? 0 : 2 * n + 1][r] * vs[h][r][NQ == 1 ? 2 * f + 1 : f];
+                  const float a = wt[u][NQ == 1 ? 0 : 2 * n][r] * vf[NQ == 1 ? 2 * f : f];
+                  const float bb = wt[u][NQ == 1 ? 0 : 2 * n + 1][r] * vf[NQ == 1 ? 2 * f + 1 : f];
                   pf[n][f][r] = transpose_8x8(h2_bits(__floats2half2_rn(a, bb)));
                 }
             }
-            const uint8_t* vrow = base + lay.codes + (x0 + (h0 + h) * 32) * HALF;
             uint32_t vc[4][VW];  // value codes of keys key0, key1, key0 + 8, key1 + 8
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const uint8_t* at = vrow + q4_code_at<D>(first + (r & 1 ? key1 : key0) + 8 * (r >> 1), g * MT);
+              const uint32_t at = base + (r & 1 ? at_val1 : at_val0) + u * next_codes + (r >> 1) * eight;
               if constexpr (D == 128) {
-                const uint2 v = *reinterpret_cast<const uint2*>(at);
+                const uint2 v = lds64(at);
                 vc[r][0] = v.x, vc[r][1] = v.y;
               } else {
-                vc[r][0] = *reinterpret_cast<const uint32_t*>(at);
+                vc[r][0] = lds32(at);
               }
             }
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+#pragma unroll
+              for (int f = 0; f < kF; ++f)
+                mma_f16(eights[n][f], {kEightsLow, kEightsHigh, kEightsLow, kEightsHigh}, pf[n][f][0], pf[n][f][1]);
 #pragma unroll
             for (int w = 0; w < VW; ++w)
 #pragma unroll
@@ -692,23 +819,17 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
                 const uint32_t a = __byte_perm(vc[0][w], vc[1][w], pick), bb = __byte_perm(vc[2][w], vc[3][w], pick);
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {  // channel tile x: byte 2y + z of word w
-                  const int x = 4 * w + 2 * y + z, grp = x * 4 / MT;
+                  const int x = 4 * w + 2 * y + z, f = NQ == 1 ? x * 2 / MT : x * 4 / MT;
                   const uint32_t az = a >> (8 * z), bz = bb >> (8 * z);
-                  const uint32_t frag[4] = {h2_bits(codes_f16<false>(az)), h2_bits(codes_f16<true>(az)),
-                                            h2_bits(codes_f16<false>(bz)), h2_bits(codes_f16<true>(bz))};
+                  const uint32_t frag[4] = {az & 0x000f000fu, az & 0x00f000f0u, bz & 0x000f000fu, bz & 0x00f000f0u};
 #pragma unroll
-                  for (int n = 0; n < NP; ++n) {
-                    const int f = NQ == 1 ? grp / 2 : grp;
-                    mma_f16(o[h][n][x], frag, pf[n][f % kF][0], pf[n][f % kF][1]);
-                  }
+                  for (int n = 0; n < NP; ++n) mma_f16(o[n][x], frag, pf[n][f][0], pf[n][f][1]);
                 }
               }
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[stage]);
-        rem += dr;
-        if (rem >= grow) rem -= grow;
         if (++stage == lay.stages) {
           stage = 0;
           phase ^= 1;
@@ -717,36 +838,59 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
 
       // Join the warps that share a head, and write the result or the partial.
 #pragma unroll
-      for (int h = 0; h < HPW; ++h)
+      for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) l[h][n] += __shfl_xor_sync(0xffffffffu, l[h][n], x);
-      key_warps_sync();  // every warp is done with the query fragments
-#pragma unroll
-      for (int h = 0; h < HPW; ++h)
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          if (g == 0) {
-            sh.red_m[warp][(h * NQ + n) * 4 + t] = m[h][n];
-            sh.red_l[warp][(h * NQ + n) * 4 + t] = l[h][n];
-          }
-          float* row = join + ((warp * HPW + h) * 4 * NQ + 4 * n + t) * D + g;
-#pragma unroll
-          for (int x = 0; x < MT; ++x) {
-            const int y = NQ == 1 ? (x * 4 / MT) & 1 : n & 1;  // the column that holds this head under this group's scales
-            row[16 * x] = o[h][n / 2][x][y];
-            row[16 * x + 8] = o[h][n / 2][x][2 + y];
-          }
-        }
-      key_warps_sync();
+        for (int x = 4; x < 32; x <<= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], x);
       const bool whole = t0 == 0 && t1 == tiles;
       const int hpb = HPB * p.group;
       const int64_t slot0 = (static_cast<int64_t>(blockIdx.x) * 2 + (cur == st.begin ? 0 : 1)) * hpb;
       float* ml = p.ws + static_cast<int64_t>(p.n_cta) * 2 * hpb * D;
-      for (int x = threadIdx.x; x < hpb * (D / 4); x += 32 * kDecodeQ4KeyWarps) {
+      if (wph == 1) {  // this warp has all of its head: straight from its registers
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          if (4 * n + t >= p.group) continue;
+          const int q = head * p.group + 4 * n + t;
+          const int64_t at = static_cast<int64_t>(b) * p.Hq + hb * hpb + q;
+          const float inv = 1.f / l[n];
+#pragma unroll
+          for (int x = 0; x < MT; ++x) {
+            const int y = NQ == 1 ? (x * 4 / MT) & 1 : n & 1, f = NQ == 1 ? x * 2 / MT : x * 4 / MT;
+            const float lo = (o[n / 2][x][y] - eights[n / 2][f][y]) * 0x1p24f;
+            const float hi = (o[n / 2][x][2 + y] - eights[n / 2][f][2 + y]) * 0x1p20f;
+            if (whole) {
+              p.out[at * D + 16 * x + g] = __float2bfloat16_rn(lo * inv);
+              p.out[at * D + 16 * x + 8 + g] = __float2bfloat16_rn(hi * inv);
+            } else {
+              p.ws[(slot0 + q) * D + 16 * x + g] = lo;
+              p.ws[(slot0 + q) * D + 16 * x + 8 + g] = hi;
+            }
+          }
+          if (g == 0) {
+            if (!whole) *reinterpret_cast<float2*>(ml + (slot0 + q) * 2) = make_float2(m[n], l[n]);
+            else if (p.lse != nullptr) p.lse[at] = (m[n] + log2f(l[n])) * 0.69314718055994531f;
+          }
+        }
+      } else {
+      key_warps_sync<KEYS>();  // every warp is done with the query fragments
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        if (g == 0) {
+          sh.red_m[warp][4 * n + t] = m[n];
+          sh.red_l[warp][4 * n + t] = l[n];
+        }
+        float* row = join + (warp * 4 * NQ + 4 * n + t) * (D + 8) + g;
+#pragma unroll
+        for (int x = 0; x < MT; ++x) {
+          const int y = NQ == 1 ? (x * 4 / MT) & 1 : n & 1;  // the column that holds this head under this group's scales
+          const int f = NQ == 1 ? x * 2 / MT : x * 4 / MT;
+          row[16 * x] = (o[n / 2][x][y] - eights[n / 2][f][y]) * 0x1p24f;
+          row[16 * x + 8] = (o[n / 2][x][2 + y] - eights[n / 2][f][2 + y]) * 0x1p20f;
+        }
+      }
+      key_warps_sync<KEYS>();
+      for (int x = threadIdx.x; x < hpb * (D / 4); x += 32 * KEYS) {
         const int q = x / (D / 4), c = x % (D / 4) * 4;  // query head of the block, its channels c .. c + 3
-        const int kv = q / p.group, in = kv % HPW * 4 * NQ + q % p.group, w0 = kv / HPW * wph;
+        const int in = q % p.group, w0 = q / p.group * wph;
         float mx = -INFINITY;
         for (int w = 0; w < wph; ++w) mx = fmaxf(mx, sh.red_m[w0 + w][in]);
         float lsum = 0.f;
@@ -758,7 +902,7 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
             continue;
           }
           const float f = ex2_approx(mw - mx);
-          const float4 v = *reinterpret_cast<const float4*>(join + ((w0 + w) * HPW * 4 * NQ + in) * D + c);
+          const float4 v = *reinterpret_cast<const float4*>(join + ((w0 + w) * 4 * NQ + in) * (D + 8) + c);
           lsum = fmaf(sh.red_l[w0 + w][in], f, lsum);
           acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
           acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
@@ -774,7 +918,8 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
           if (c == 0) *reinterpret_cast<float2*>(ml + (slot0 + q) * 2) = make_float2(mx, lsum);
         }
       }
-      key_warps_sync();  // the region is free for the next segment's query
+      }
+      key_warps_sync<KEYS>();  // the region is free for the next segment's query
     }
     cur += t1 - t0;
     t0 = 0;
@@ -789,59 +934,55 @@ constexpr int kCombineQ4Threads = 256;
 
 // Joins the partials of one (entry, query head), which lie in the ranges of CTAs c0 .. c1;
 // writes zeros and -inf for an empty entry, NaN for a length outside the contract (reported
-// by jl_sync_status) or a kernel that gave up.  Every thread asks for all it needs before it
-// waits for any of it: thread c for the maximum and sum of partial c0 + c, lane by lane the
-// channels of every eighth partial.  One round trip for up to 148 partials.
-template <int D>
+// by jl_sync_status) or a kernel that gave up.  Every thread asks for what it needs before it
+// waits for any of it: thread c for the maximum and sum of partial c0 + c, and the channels
+// of its first partials.  SPLIT blocks share a head, each a part of its channels: with few
+// heads to join, one block a head left 32 SMs to fetch 77 KB each (3.2 us against 0.9).
+template <int D, int SPLIT>
 __global__ void __launch_bounds__(kCombineQ4Threads) jl_decode_q4_combine_kernel(const DecodeQ4Params p) {
-  constexpr int NW = kCombineQ4Threads / 32, CPL = D / 32, PER = (kDecodeQ4Ctas + NW - 1) / NW;
+  constexpr int NW = kCombineQ4Threads / 32, CH = D / SPLIT, LANES = CH / 4;  // a float4 a lane
+  constexpr int ROWS = kCombineQ4Threads / LANES, PER = 5;                    // partials at a time, and rounds in flight
   static_assert(kDecodeQ4Ctas <= kCombineQ4Threads, "a thread for each partial");
-  __shared__ float weight[kCombineQ4Threads], red[2][NW], sum[NW][D];
-  const int qh = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float weight[kCombineQ4Threads], red[2][NW];
+  __shared__ __align__(16) float sum[ROWS][CH];
+  const int qh = blockIdx.x / SPLIT, ch = blockIdx.x % SPLIT * CH + threadIdx.x % LANES * 4, row = threadIdx.x / LANES;
+  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_launch_dependents();
-  griddep_wait();
+  // The decode lets this kernel start only after it waited for everything before it, so the
+  // lengths are there; its own partials and the status word are there after the wait.
   const int hpb = p.heads_per_block * p.group, hb = qh / hpb;
   const int L = p.seqlens[b], t = q4_tiles(p, L);
-  const int2 n = q4_tiles_before(p, b, lane);
-  const bool wrong = L < 0 || L > p.max_seqlen;
-  const bool bad = wrong || status_failed();
-  const int64_t at = static_cast<int64_t>(b) * p.Hq + qh;
-  if (__syncthreads_or(bad) || t == 0) {
-    if (wrong && threadIdx.x == 0 && qh == 0) atomicOr(&g_status, kDevErrBounds);
-    const bool nan = bad || t != 0;
-    const float x = nan ? __int_as_float(0x7fc00000) : 0.f;
-    for (int c = threadIdx.x; c < D; c += kCombineQ4Threads) p.out[at * D + c] = __float2bfloat16_rn(x);
-    if (threadIdx.x == 0 && p.lse != nullptr) p.lse[at] = nan ? x : -INFINITY;
-    return;
-  }
-  const int64_t total = static_cast<int64_t>(n.x) * (p.Hkv / p.heads_per_block);
-  const int64_t first = static_cast<int64_t>(hb) * n.x + n.y;
+  int unused;
+  const int2 n = q4_tiles_before(p, b, lane, unused);
+  const int total = n.x * (p.Hkv / p.heads_per_block), first = hb * n.x + n.y;
   const int n_cta = q4_ctas(p, total);
-  const int c0 = q4_cta_of(total, n_cta, first), c1 = q4_cta_of(total, n_cta, first + t - 1);
-  if (c0 == c1) return;  // the decode wrote the result
-  const int s0 = q4_range_begin(total, n_cta, c0) == first ? 0 : 1;
-  const int count = c1 - c0 + 1;
+  const int c0 = t ? q4_cta_of(total, n_cta, first) : 0, c1 = t ? q4_cta_of(total, n_cta, first + t - 1) : 0;
+  const int s0 = t && q4_range_begin(total, n_cta, c0) == first ? 0 : 1;
+  const int count = c1 > c0 ? c1 - c0 + 1 : 0;  // 0: the decode wrote the result, or there is none
   auto slot = [&](int c) { return ((c0 + c) * 2LL + (c == 0 ? s0 : 0)) * hpb + qh % hpb; };
   const float* ml = p.ws + static_cast<int64_t>(p.n_cta) * 2 * hpb * D;
+  griddep_wait();
+  const bool wrong = L < 0 || L > p.max_seqlen;
+  const bool bad = wrong || status_failed();
   float2 own = make_float2(-INFINITY, 0.f);
   if (threadIdx.x < count) own = *reinterpret_cast<const float2*>(ml + slot(threadIdx.x) * 2);
-  float o[PER][CPL];
+  float4 o[PER];
+  auto ask = [&](int c) {
 #pragma unroll
-  for (int u = 0; u < PER; ++u) {
-    const int c = warp + u * NW;
-#pragma unroll
-    for (int e = 0; e < CPL; ++e) o[u][e] = 0.f;
-    if (c < count) {
-      const float* row = p.ws + slot(c) * D + lane * CPL;
-      if constexpr (CPL == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(row);
-        o[u][0] = x.x, o[u][1] = x.y, o[u][2] = x.z, o[u][3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(row);
-        o[u][0] = x.x, o[u][1] = x.y;
-      }
-    }
+    for (int u = 0; u < PER; ++u)
+      if (c + u * ROWS < count) o[u] = *reinterpret_cast<const float4*>(p.ws + slot(c + u * ROWS) * D + ch);
+  };
+  ask(row);
+  const int64_t at = static_cast<int64_t>(b) * p.Hq + qh;
+  if (__syncthreads_or(bad) || t == 0) {
+    if (wrong && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(&g_status, kDevErrBounds);
+    const bool nan = bad || t != 0;
+    const float x = nan ? __int_as_float(0x7fc00000) : 0.f;
+    if (row == 0) *reinterpret_cast<uint2*>(p.out + at * D + ch) = make_uint2(pack_bf16x2(x, x), pack_bf16x2(x, x));
+    if (threadIdx.x == 0 && blockIdx.x % SPLIT == 0 && p.lse != nullptr) p.lse[at] = nan ? x : -INFINITY;
+    return;
   }
+  if (count == 0) return;
   float mx = own.x;
 #pragma unroll
   for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
@@ -857,29 +998,30 @@ __global__ void __launch_bounds__(kCombineQ4Threads) jl_decode_q4_combine_kernel
   for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
   if (lane == 0) red[1][warp] = l;
   __syncthreads();
-  float acc[CPL];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = row; c < count; c += PER * ROWS) {
+    if (c != row) ask(c);
 #pragma unroll
-  for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
-#pragma unroll
-  for (int u = 0; u < PER; ++u) {
-    if (warp + u * NW >= count) break;
-    const float w = weight[warp + u * NW];
-#pragma unroll
-    for (int e = 0; e < CPL; ++e) acc[e] = fmaf(o[u][e], w, acc[e]);
+    for (int u = 0; u < PER; ++u) {
+      if (c + u * ROWS >= count) break;
+      const float w = weight[c + u * ROWS];
+      acc.x = fmaf(o[u].x, w, acc.x), acc.y = fmaf(o[u].y, w, acc.y);
+      acc.z = fmaf(o[u].z, w, acc.z), acc.w = fmaf(o[u].w, w, acc.w);
+    }
   }
-#pragma unroll
-  for (int e = 0; e < CPL; ++e) sum[warp][lane * CPL + e] = acc[e];
+  *reinterpret_cast<float4*>(&sum[row][threadIdx.x % LANES * 4]) = acc;
   __syncthreads();
   l = 0.f;
 #pragma unroll
   for (int w = 0; w < NW; ++w) l += red[1][w];
-  if (threadIdx.x < D) {
+  if (threadIdx.x < CH) {
     float x = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) x += sum[w][threadIdx.x];
-    p.out[at * D + threadIdx.x] = __float2bfloat16_rn(x / l);
+#pragma unroll 8
+    for (int r = 0; r < min(ROWS, count); ++r) x += sum[r][threadIdx.x];
+    p.out[at * D + blockIdx.x % SPLIT * CH + threadIdx.x] = __float2bfloat16_rn(x / l);
   }
-  if (threadIdx.x == 0 && p.lse != nullptr) p.lse[at] = (mx + log2f(l)) * 0.69314718055994531f;
+  if (threadIdx.x == 0 && blockIdx.x % SPLIT == 0 && p.lse != nullptr)
+    p.lse[at] = (mx + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace jl

@@ -41,7 +41,7 @@ def test_decode_refuses_before_launching(jl, over, status):
 
 
 @pytest.mark.parametrize("over,status", [
-    (dict(page=100), 2), (dict(page=16), 2), (dict(page=0), 2), (dict(max_pages=7), 1), (dict(max_pages=0), 1),
+    (dict(page=100), 2), (dict(page=8), 2), (dict(page=0), 2), (dict(max_pages=7), 1), (dict(max_pages=0), 1),
     (dict(pages=0), 1), (dict(pages=1 << 24), 1), (dict(table=None), 1), (dict(vc=8), 1),
 ])
 def test_paged_decode_refuses_before_launching(jl, over, status):
