@@ -610,11 +610,13 @@ jl_status q4_common(Q4Op op, jl::Q4Params& prm, int64_t rows, int32_t head_dim, 
                              prm.v_out, prm.cos_tab, prm.sin_tab};
   for (const void* x : all)
     if (!aligned16(x)) return fail(JL_ERR_INVALID, "every tensor must be 16-byte aligned");
-  const int64_t per = op == Q4Op::kFill ? prm.Hkv : op == Q4Op::kAppend ? prm.Hq + prm.Hkv : prm.Hkv;
-  const int64_t n = op == Q4Op::kRead ? prm.batch * rows : rows;
-  if (n > 0x7fffffffLL || n * per > 8 * 0x7fffffffLL)
-    return fail(JL_ERR_UNSUPPORTED, "too many rows for one call (%lld)", (long long)n);
-  const unsigned blocks = static_cast<unsigned>((n * per + 7) / 8);
+  // rows of (token, head), four lanes each; an append's queries take a warp each before them
+  const int64_t tokens = op != Q4Op::kRead ? rows : rows > 0x7fffffffLL ? rows : prm.batch * rows;
+  const int64_t n = tokens > 0x7fffffffLL ? 0 : tokens * prm.Hkv;
+  const int64_t lanes = op == Q4Op::kAppend ? 32 * (tokens * prm.Hq + (n + 7) / 8) : 4 * n;
+  if (tokens > 0x7fffffffLL || lanes > 0x7fffffffLL * 256)
+    return fail(JL_ERR_UNSUPPORTED, "too many rows for one call (%lld)", (long long)tokens);
+  const unsigned blocks = static_cast<unsigned>((lanes + 255) / 256);
   const bool wide = head_dim == 128;
   if (op == Q4Op::kFill) {
     if (wide) jl::jl_kv_fill_q4_kernel<128><<<blocks, 256, 0, st>>>(prm);

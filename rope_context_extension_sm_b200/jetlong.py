@@ -463,70 +463,82 @@ def jl_kv_cache_q4_empty(n: int, stride: int, n_kv_heads: int, head_dim: int, *,
     return codes[0], codes[1], torch.empty((n, stride, n_kv_heads, 8), dtype=torch.bfloat16, device=device)
 
 
-def _q4_cache(k_codes, v_codes, scales, block_table=None):
-    """Checks the three tensors (and a block table); returns (Hkv, head_dim)."""
-    _need(k_codes, torch.uint8, "k_codes", 4)
-    _need(v_codes, torch.uint8, "v_codes", 4)
-    _need(scales, torch.bfloat16, "scales", 4)
-    if v_codes.shape != k_codes.shape or scales.shape != (*k_codes.shape[:3], 8):
-        raise ValueError("k_codes and v_codes must be [B][stride][Hkv][d/2] and scales [B][stride][Hkv][8]")
-    if block_table is not None:
-        _need(block_table, torch.int32, "block_table", 2)
-    return k_codes.shape[2], 2 * k_codes.shape[3]
+# The checks below run for every token that a serving loop decodes, so each tensor is checked in one
+# expression, and only a failed one is looked at again for its message.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _q4_shape(t: torch.Tensor, name: str, shape: tuple, dtype=torch.bfloat16) -> None:
+def _q4_bad(t, dtype, shape, dev, name):
+    """Raises what is wrong with a tensor that has to have this type, shape and device."""
     _need(t, dtype, name, len(shape))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, the cache is on cuda:{dev}")
 
 
-def _q4_tables(cos, sin, d: int) -> None:
-    _need(cos, torch.float32, "cos", 2)
-    _need(sin, torch.float32, "sin", 2)
-    if cos.shape != sin.shape or cos.shape[1] != d // 2:
-        raise ValueError("cos and sin must both be [n_pos][head_dim/2]")
+def _q4_is(t, dtype, shape, dev, name) -> int:
+    """Checks a tensor and returns its address."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _q4_bad(t, dtype, shape, dev, name)
+    return t.data_ptr()
 
 
-def _q4_alloc(stream, device):
-    """Context in which outputs and workspaces are allocated: the stream that the call runs on, so
-    that the allocator does not hand their memory to another stream's work meanwhile."""
-    if stream is None:
-        return contextlib.nullcontext()
+def _q4_cache(k_codes, v_codes, scales, block_table, batch: int):
+    """Checks a cache (or a pool and its block table) for `batch` entries.  Returns its device, Hkv,
+    head_dim, the three addresses, and where an entry's rows are: (stride,) or (table, max_pages,
+    page_size, num_pages)."""
+    shape, dev = k_codes.shape, k_codes.get_device()
+    if len(shape) != 4 or dev < 0:
+        _need(k_codes, _U8, "k_codes", 4)
+    n, rows, hkv, half = shape
+    at = (_q4_is(k_codes, _U8, shape, dev, "k_codes"), _q4_is(v_codes, _U8, shape, dev, "v_codes"),
+          _q4_is(scales, _BF16, (n, rows, hkv, 8), dev, "scales"))
+    if block_table is None:
+        if n != batch:
+            raise ValueError(f"the cache must have one entry for each of the {batch} sequences (it has {n})")
+        return dev, hkv, 2 * half, at, (rows,)
+    table = block_table.shape
+    if len(table) != 2 or table[0] != batch:
+        raise ValueError(f"block_table must be [{batch}][max_pages] (got {tuple(table)})")
+    return dev, hkv, 2 * half, at, (_q4_is(block_table, _I32, table, dev, "block_table"), table[1], rows, n)
+
+
+def _q4_tables(cos, sin, d: int, dev: int):
+    shape = (cos.shape[0], d // 2)
+    return _q4_is(cos, _F32, shape, dev, "cos"), _q4_is(sin, _F32, shape, dev, "sin"), shape[0]
+
+
+def _q4_alloc(stream, dev: int):
+    """Context in which outputs and workspaces for another stream than the current one are allocated:
+    that stream, so that the allocator does not hand their memory to other work meanwhile."""
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+        stream = torch.cuda.ExternalStream(_stream(stream), device=dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the cache is on cuda:{dev}")
     return torch.cuda.stream(stream)
 
 
-def _q4_call(name: str, stream, tensors, *args) -> None:
-    """Calls the entry point on the tensors' device (all on one) and that device's current
-    stream unless one is given."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: the tensors are on different devices ({dev} and {t.device})")
-    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
-        raise ValueError(f"{name}: the stream belongs to {stream.device}, the tensors are on {dev}")
-    with torch.cuda.device(dev):
-        _check(getattr(_lib, name)(*args, _stream(stream)), name)
+def _q4_call(name: str, stream, dev: int, *args) -> None:
+    """Calls the entry point on the tensors' device, on the stream given or that device's current one."""
+    raw = _raw_stream(dev) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == dev:
+        status = getattr(_lib, name)(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(_lib, name)(*args, raw)
+    if status:
+        _check(status, name)
 
 
 def _fill_q4(name, k, v, cu_seqlens, cos, sin, k_codes, v_codes, scales, past_lens, stream, block_table):
-    hkv, d = _q4_cache(k_codes, v_codes, scales, block_table)
-    T, batch = k.shape[0], cu_seqlens.shape[0] - 1
-    _q4_shape(k, "k", (T, hkv, d))
-    _q4_shape(v, "v", (T, hkv, d))
-    _q4_tables(cos, sin, d)
-    _need(cu_seqlens, torch.int32, "cu_seqlens", 1)
-    if past_lens is not None:
-        _q4_shape(past_lens, "past_lens", (batch,), torch.int32)
-    if block_table is None and k_codes.shape[0] != batch or block_table is not None and block_table.shape[0] != batch:
-        raise ValueError(f"the cache or the block table must have one entry for each of the {batch} sequences")
-    where = (k_codes.shape[1],) if block_table is None else (_ptr(block_table), block_table.shape[1], k_codes.shape[1],
-                                                             k_codes.shape[0])
-    _q4_call(name, stream, (k, v, cu_seqlens, past_lens, cos, sin, k_codes, v_codes, scales, block_table),
-             _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(past_lens), batch, T, hkv, d, _ptr(cos), _ptr(sin),
-             cos.shape[0], _ptr(k_codes), _ptr(v_codes), _ptr(scales), *where)
+    batch = cu_seqlens.shape[0] - 1
+    dev, hkv, d, cache, where = _q4_cache(k_codes, v_codes, scales, block_table, batch)
+    T = k.shape[0]
+    _q4_call(name, stream, dev, _q4_is(k, _BF16, (T, hkv, d), dev, "k"), _q4_is(v, _BF16, (T, hkv, d), dev, "v"),
+             _q4_is(cu_seqlens, _I32, (batch + 1,), dev, "cu_seqlens"),
+             None if past_lens is None else _q4_is(past_lens, _I32, (batch,), dev, "past_lens"), batch, T, hkv, d,
+             *_q4_tables(cos, sin, d, dev), *cache, *where)
     return k_codes, v_codes, scales
 
 
@@ -545,25 +557,20 @@ def jl_kv_cache_fill_q4_paged(k, v, cu_seqlens, cos, sin, k_codes, v_codes, scal
 
 
 def _append_q4(name, q, k, v, seqlens, cos, sin, k_codes, v_codes, scales, q_out, stream, block_table):
-    hkv, d = _q4_cache(k_codes, v_codes, scales, block_table)
-    _need(q, torch.bfloat16, "q", 3)
-    B, hq = q.shape[:2]
-    _q4_shape(q, "q", (B, hq, d))
-    _q4_shape(k, "k", (B, hkv, d))
-    _q4_shape(v, "v", (B, hkv, d))
-    _q4_shape(seqlens, "seqlens", (B,), torch.int32)
-    _q4_tables(cos, sin, d)
+    shape = q.shape
+    if len(shape) != 3:
+        _need(q, _BF16, "q", 3)
+    B, hq = shape[:2]
+    dev, hkv, d, cache, where = _q4_cache(k_codes, v_codes, scales, block_table, B)
     if q_out is None:
-        with _q4_alloc(stream, q.device):
+        if stream is None:
             q_out = torch.empty_like(q)
-    _q4_shape(q_out, "q_out", (B, hq, d))
-    if block_table is None and k_codes.shape[0] != B or block_table is not None and block_table.shape[0] != B:
-        raise ValueError(f"the cache or the block table must have one entry for each of the {B} tokens")
-    where = (k_codes.shape[1],) if block_table is None else (_ptr(block_table), block_table.shape[1], k_codes.shape[1],
-                                                             k_codes.shape[0])
-    _q4_call(name, stream, (q, k, v, seqlens, cos, sin, q_out, k_codes, v_codes, scales, block_table),
-             _ptr(q), _ptr(k), _ptr(v), _ptr(seqlens), B, hq, hkv, d, _ptr(cos), _ptr(sin), cos.shape[0],
-             _ptr(q_out), _ptr(k_codes), _ptr(v_codes), _ptr(scales), *where)
+        else:
+            with _q4_alloc(stream, dev):
+                q_out = torch.empty_like(q)
+    _q4_call(name, stream, dev, _q4_is(q, _BF16, (B, hq, d), dev, "q"), _q4_is(k, _BF16, (B, hkv, d), dev, "k"),
+             _q4_is(v, _BF16, (B, hkv, d), dev, "v"), _q4_is(seqlens, _I32, (B,), dev, "seqlens"), B, hq, hkv, d,
+             *_q4_tables(cos, sin, d, dev), _q4_is(q_out, _BF16, shape, dev, "q_out"), *cache, *where)
     return q_out
 
 
@@ -581,29 +588,20 @@ def jl_decode_append_q4_paged(q, k, v, seqlens, cos, sin, k_codes, v_codes, scal
 
 
 def _read_q4(name, k_codes, v_codes, scales, lens, starts, k_out, v_out, rows, stream, block_table):
-    hkv, d = _q4_cache(k_codes, v_codes, scales, block_table)
-    _need(lens, torch.int32, "lens", 1)
     B = lens.shape[0]
-    if starts is not None:
-        _q4_shape(starts, "starts", (B,), torch.int32)
-    if block_table is None and k_codes.shape[0] != B or block_table is not None and block_table.shape[0] != B:
-        raise ValueError(f"the cache or the block table must have one entry for each of the {B} lengths")
+    dev, hkv, d, cache, where = _q4_cache(k_codes, v_codes, scales, block_table, B)
     if rows is None:
         given = k_out if k_out is not None else v_out
-        stride = k_codes.shape[1] * (1 if block_table is None else block_table.shape[1])
-        rows = given.shape[1] if given is not None else stride
-    with _q4_alloc(stream, k_codes.device):
-        if k_out is None:
-            k_out = torch.empty((B, rows, hkv, d), dtype=torch.bfloat16, device=k_codes.device)
-        if v_out is None:
-            v_out = torch.empty((B, rows, hkv, d), dtype=torch.bfloat16, device=k_codes.device)
-    _q4_shape(k_out, "k_out", (B, rows, hkv, d))
-    _q4_shape(v_out, "v_out", (B, rows, hkv, d))
-    where = (k_codes.shape[1],) if block_table is None else (_ptr(block_table), block_table.shape[1], k_codes.shape[1],
-                                                             k_codes.shape[0])
-    _q4_call(name, stream, (k_codes, v_codes, scales, lens, starts, k_out, v_out, block_table),
-             _ptr(k_codes), _ptr(v_codes), _ptr(scales), *where, _ptr(starts), _ptr(lens), B, hkv, d, _ptr(k_out),
-             _ptr(v_out), rows)
+        rows = given.shape[1] if given is not None else where[0] if block_table is None else where[1] * where[2]
+    shape = (B, rows, hkv, d)
+    if k_out is None or v_out is None:
+        with contextlib.nullcontext() if stream is None else _q4_alloc(stream, dev):
+            k_out = torch.empty(shape, dtype=_BF16, device=k_codes.device) if k_out is None else k_out
+            v_out = torch.empty(shape, dtype=_BF16, device=k_codes.device) if v_out is None else v_out
+    _q4_call(name, stream, dev, *cache, *where,
+             None if starts is None else _q4_is(starts, _I32, (B,), dev, "starts"),
+             _q4_is(lens, _I32, (B,), dev, "lens"), B, hkv, d, _q4_is(k_out, _BF16, shape, dev, "k_out"),
+             _q4_is(v_out, _BF16, shape, dev, "v_out"), rows)
     return k_out, v_out
 
 
@@ -628,33 +626,26 @@ def jl_bifocal_decode_q4_workspace_size(Hq: int, head_dim: int) -> int:
 
 def _decode_q4(name, q, k_codes, v_codes, scales, seqlens, max_seqlen, w0, w_pretrained, cos, sin, softmax_scale, out,
                lse, workspace, want_lse, stream, block_table):
-    hkv, d = _q4_cache(k_codes, v_codes, scales, block_table)
-    _need(q, torch.bfloat16, "q", 3)
-    B, hq = q.shape[:2]
-    _q4_shape(q, "q", (B, hq, d))
-    _q4_shape(seqlens, "seqlens", (B,), torch.int32)
-    _q4_tables(cos, sin, d)
-    if block_table is None and k_codes.shape[0] != B or block_table is not None and block_table.shape[0] != B:
-        raise ValueError(f"the cache or the block table must have one entry for each of the {B} queries")
-    with _q4_alloc(stream, q.device):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty((B, hq), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(jl_bifocal_decode_q4_workspace_size(hq, d), dtype=torch.uint8, device=q.device)
-    _q4_shape(out, "out", (B, hq, d))
-    if lse is not None:
-        _q4_shape(lse, "lse", (B, hq), torch.float32)
-    if not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    if block_table is None:
-        where = (_ptr(seqlens), B, k_codes.shape[1])
-    else:
-        where = (_ptr(block_table), _ptr(seqlens), B, block_table.shape[1], k_codes.shape[1], k_codes.shape[0])
-    _q4_call(name, stream, (q, k_codes, v_codes, scales, seqlens, cos, sin, out, lse, workspace, block_table),
-             _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(scales), *where, max_seqlen, hq, hkv, d, w0, w_pretrained,
-             _ptr(cos), _ptr(sin), cos.shape[0], softmax_scale, _ptr(out), _ptr(lse), _ptr(workspace),
+    shape = q.shape
+    if len(shape) != 3:
+        _need(q, _BF16, "q", 3)
+    B, hq = shape[:2]
+    dev, hkv, d, cache, where = _q4_cache(k_codes, v_codes, scales, block_table, B)
+    if out is None or workspace is None or (lse is None and want_lse):
+        with contextlib.nullcontext() if stream is None else _q4_alloc(stream, dev):
+            if out is None:
+                out = torch.empty_like(q)
+            if lse is None and want_lse:
+                lse = torch.empty((B, hq), dtype=_F32, device=q.device)
+            if workspace is None:
+                workspace = torch.empty(_lib.jl_bifocal_decode_q4_workspace_size(hq, d), dtype=_U8, device=q.device)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the cache's device")
+    lens = _q4_is(seqlens, _I32, (B,), dev, "seqlens")
+    where = (lens, B, *where) if block_table is None else (where[0], lens, B, *where[1:])
+    _q4_call(name, stream, dev, _q4_is(q, _BF16, (B, hq, d), dev, "q"), *cache, *where, max_seqlen, hq, hkv, d, w0,
+             w_pretrained, *_q4_tables(cos, sin, d, dev), softmax_scale, _q4_is(out, _BF16, shape, dev, "out"),
+             None if lse is None else _q4_is(lse, _F32, (B, hq), dev, "lse"), workspace.data_ptr(),
              workspace.numel() * workspace.element_size())
     return out, lse
 

@@ -483,6 +483,6 @@ def test_wrong_devices_shapes_and_strides_are_refused(jl):
     with pytest.raises(ValueError, match="shape"):
         jl.jl_kv_cache_read_q4(*cache, dev([8], torch.int32), starts=dev([0, 0], torch.int32))
     with pytest.raises(ValueError, match="contiguous"):
-        jl.jl_kv_cache_read_q4(cache[0].transpose(1, 2), *cache[1:], dev([8], torch.int32))
+        jl.jl_kv_cache_read_q4(cache[0].flip(1)[:, ::2], cache[1][:, ::2], cache[2][:, ::2], dev([8], torch.int32))
     with pytest.raises(ValueError, match="one entry"):
         jl.jl_kv_cache_read_q4(*cache, dev([8, 8], torch.int32))
