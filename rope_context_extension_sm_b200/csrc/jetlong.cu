@@ -614,7 +614,7 @@ jl_status q4_common(Q4Op op, jl::Q4Params& prm, int64_t rows, int32_t head_dim, 
   const int64_t tokens = op != Q4Op::kRead ? rows : rows > 0x7fffffffLL ? rows : prm.batch * rows;
   const int64_t n = tokens > 0x7fffffffLL ? 0 : tokens * prm.Hkv;
   const int64_t lanes = op == Q4Op::kAppend ? 32 * (tokens * prm.Hq + (n + 7) / 8) : 4 * n;
-  if (tokens > 0x7fffffffLL || lanes > 0x7fffffffLL * 256)
+  if (tokens > 0x7fffffffLL || lanes > 0x7fffffffLL * 256 || (op == Q4Op::kRead && prm.batch > 65535))
     return fail(JL_ERR_UNSUPPORTED, "too many rows for one call (%lld)", (long long)tokens);
   const unsigned blocks = static_cast<unsigned>((lanes + 255) / 256);
   const bool wide = head_dim == 128;
@@ -625,8 +625,9 @@ jl_status q4_common(Q4Op op, jl::Q4Params& prm, int64_t rows, int32_t head_dim, 
     if (wide) jl::jl_decode_append_q4_kernel<128><<<blocks, 256, 0, st>>>(prm);
     else jl::jl_decode_append_q4_kernel<64><<<blocks, 256, 0, st>>>(prm);
   } else {
-    if (wide) jl::jl_kv_read_q4_kernel<128><<<blocks, 256, 0, st>>>(prm);
-    else jl::jl_kv_read_q4_kernel<64><<<blocks, 256, 0, st>>>(prm);
+    const dim3 grid(static_cast<unsigned>((4 * rows * prm.Hkv + 255) / 256), prm.batch);
+    if (wide) jl::jl_kv_read_q4_kernel<128><<<grid, 256, 0, st>>>(prm);
+    else jl::jl_kv_read_q4_kernel<64><<<grid, 256, 0, st>>>(prm);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "4-bit cache launch");

@@ -60,9 +60,10 @@ struct Q4Params {
 // page index is outside the pool.
 __device__ __forceinline__ int64_t q4_row(const Q4Params& p, int b, int64_t pos) {
   if (p.block_table == nullptr) return static_cast<int64_t>(b) * p.cache_stride + pos;
-  const int32_t page = p.block_table[static_cast<int64_t>(b) * p.max_pages + pos / p.page_size];
+  const uint32_t x = static_cast<uint32_t>(pos), n = x / p.page_size;  // positions are below 2^31
+  const int32_t page = p.block_table[static_cast<int64_t>(b) * p.max_pages + n];
   if (page < 0 || page >= p.num_pages) return -1;
-  return static_cast<int64_t>(page) * p.page_size + pos % p.page_size;
+  return static_cast<int64_t>(page) * p.page_size + (x - n * p.page_size);
 }
 
 // The scale of a group from the largest |x| of it, given as float bits (so that a NaN or an
@@ -243,6 +244,17 @@ __device__ __forceinline__ void q4_write_row(const Q4Params& p, bool live, const
 
 constexpr int kQ4Teams = 64;  // rows of a block of 256 threads
 
+// row = token * Hkv + h, in 32 bits where it fits (a 64-bit division costs some 100 instructions).
+__device__ __forceinline__ int64_t q4_split(int64_t row, int Hkv, int& h) {
+  if (row <= 0xffffffffLL) {
+    const uint32_t r = static_cast<uint32_t>(row), t = r / static_cast<uint32_t>(Hkv);
+    h = static_cast<int>(r - t * Hkv);
+    return t;
+  }
+  h = static_cast<int>(row % Hkv);
+  return row / Hkv;
+}
+
 // Prompt tokens: token t of sequence b goes to position past[b] + t - cu_seqlens[b].
 template <int D>
 __global__ void __launch_bounds__(4 * kQ4Teams) jl_kv_fill_q4_kernel(const Q4Params p) {
@@ -252,8 +264,7 @@ __global__ void __launch_bounds__(4 * kQ4Teams) jl_kv_fill_q4_kernel(const Q4Par
   int64_t pos = 0, crow = 0;
   int h = 0;
   if (live) {
-    const int64_t t = row / p.Hkv;
-    h = static_cast<int>(row % p.Hkv);
+    const int64_t t = q4_split(row, p.Hkv, h);
     int lo = 0, hi = p.batch - 1;  // sequence holding token t: last b with cu[b] <= t
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -298,8 +309,9 @@ __global__ void __launch_bounds__(4 * kQ4Teams) jl_decode_append_q4_kernel(const
   const int w = lane & 3;
   bool live = row < static_cast<int64_t>(p.batch) * p.Hkv;
   int64_t i = 0, crow = 0;
+  int h = 0;
   if (live) {
-    const int b = static_cast<int>(row / p.Hkv);
+    const int b = static_cast<int>(q4_split(row, p.Hkv, h));
     i = static_cast<int64_t>(p.lens[b]) - 1;
     crow = (i < 0 || i >= p.cache_stride || i >= p.n_tab_rows) ? -1 : q4_row(p, b, i);
     if (crow < 0) {
@@ -307,7 +319,7 @@ __global__ void __launch_bounds__(4 * kQ4Teams) jl_decode_append_q4_kernel(const
       live = false;
     }
   }
-  q4_write_row<D>(p, live, p.k + row * D, p.v + row * D, i, crow, static_cast<int>(row % p.Hkv), w);
+  q4_write_row<D>(p, live, p.k + row * D, p.v + row * D, i, crow, h, w);
 }
 
 // 16-byte chunks 0 and 1 of lane w, which fill one 32-byte sector each two, change places with
@@ -336,22 +348,25 @@ __device__ __forceinline__ uint32_t q4_values(uint32_t word, int i, __nv_bfloat1
 template <int D>
 __global__ void __launch_bounds__(4 * kQ4Teams) jl_kv_read_q4_kernel(const Q4Params p) {
   constexpr int HALF = D / 2, NP = D / 8;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kQ4Teams + threadIdx.x / 4;
-  const int w = threadIdx.x & 3;
-  bool live = row < static_cast<int64_t>(p.batch) * p.out_rows * p.Hkv;
+  const int b = blockIdx.y, w = threadIdx.x & 3;
+  const int64_t first = p.past != nullptr ? p.past[b] : 0, len = p.lens[b];
+  if (first < 0 || len > p.cache_stride || len - first > p.out_rows) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(&g_status, kDevErrBounds);
+    return;
+  }
+  if (static_cast<int64_t>(blockIdx.x) * kQ4Teams >= (len - first) * p.Hkv) return;
+  const int64_t in_entry = static_cast<int64_t>(blockIdx.x) * kQ4Teams + threadIdx.x / 4;  // row of this entry
+  int h;
+  const int64_t pos = first + q4_split(in_entry, p.Hkv, h), row = b * p.out_rows * p.Hkv + in_entry;
+  bool live = pos < len;
   int64_t r = 0;
   if (live) {
-    const int64_t br = row / p.Hkv;
-    const int b = static_cast<int>(br / p.out_rows);
-    const int64_t first = p.past != nullptr ? p.past[b] : 0, pos = first + br % p.out_rows, len = p.lens[b];
-    const bool wrong = first < 0 || len > p.cache_stride || len - first > p.out_rows;
-    live = !wrong && pos < len;
-    const int64_t crow = live ? q4_row(p, b, pos) : 0;
-    if (wrong || crow < 0) {
+    const int64_t crow = q4_row(p, b, pos);
+    if (crow < 0) {
       if (w == 0) atomicOr(&g_status, kDevErrBounds);
       live = false;
     }
-    r = crow * p.Hkv + row % p.Hkv;
+    r = crow * p.Hkv + h;
   }
   uint4 kw = make_uint4(0u, 0u, 0u, 0u), vw = kw;  // this lane's quarter of the codes
   uint32_t ks = 0, vs = 0;
