@@ -718,7 +718,7 @@ jl_status make_q4_map(CUtensorMap* map, const void* base, int64_t rows, int grou
   return JL_OK;
 }
 
-template <int D, int NQ, int KEYS>
+template <int D, int NQ, int KEYS, int U>
 jl_status launch_decode_q4(const jl::DecodeQ4Params& prm, cudaStream_t st) {
   const int64_t rows = prm.block_table != nullptr ? static_cast<int64_t>(prm.num_pages) * prm.page_size
                                                   : prm.B * prm.cache_stride;
@@ -729,7 +729,7 @@ jl_status launch_decode_q4(const jl::DecodeQ4Params& prm, cudaStream_t st) {
   if ((s = make_q4_map(&tv, prm.v_codes, rows, groups, width, hpb * (D / 2) / width)) != JL_OK) return s;
   if ((s = make_q4_map(&ts, prm.scales, rows, prm.Hkv / hpb, 16 * hpb, 1)) != JL_OK) return s;
   const int smem = jl::decode_q4_layout(D, NQ, KEYS, prm.heads_per_block, prm.tile).total;
-  auto kern = jl::jl_decode_q4_kernel<D, NQ, KEYS>;
+  auto kern = jl::jl_decode_q4_kernel<D, NQ, KEYS, U>;
   const KernelAttr attr = kernel_attr(reinterpret_cast<const void*>(kern), 222 * 1024);
   if (attr.err != cudaSuccess) return cuda_fail(attr.err, "cudaFuncSetAttribute(4-bit decode)");
   if (attr.regs < jl::DecodeQ4Warps<KEYS>::kRegs)  // setmaxnreg draws on the launch's registers and would wait for good
@@ -752,15 +752,15 @@ jl_status dispatch_decode_q4(jl::DecodeQ4Params& prm, cudaStream_t st) {
   const int nq = prm.group <= 4 ? 1 : prm.group <= 8 ? 2 : 4;
   int hpb = 8 / nq;
   while (prm.Hkv % hpb != 0) hpb /= 2;
-  const int keys = 8;
+  const int sixteens = nq > 1 ? 1 : hpb == 8 ? 4 : 2;
   prm.heads_per_block = hpb;
-  prm.tile = (nq == 1 ? 16 * Q4_U : 16) * keys / hpb;
+  prm.tile = 16 * sixteens * 8 / hpb;
   const int64_t tiles = (static_cast<int64_t>(prm.max_seqlen) + prm.tile - 1) / prm.tile * prm.B * (prm.Hkv / hpb);
   if (tiles > 0x7fffffff) return fail(JL_ERR_UNSUPPORTED, "too many keys for one call (%lld tiles)", (long long)tiles);
   prm.n_cta = static_cast<int32_t>(std::min<int64_t>(jl::kDecodeQ4Ctas, tiles));
-  if (nq == 4) return launch_decode_q4<D, 4, 8>(prm, st);
-  if (nq == 2) return launch_decode_q4<D, 2, 8>(prm, st);
-  return launch_decode_q4<D, 1, 8>(prm, st);
+  if (nq == 4) return launch_decode_q4<D, 4, 8, 1>(prm, st);
+  if (nq == 2) return launch_decode_q4<D, 2, 8, 1>(prm, st);
+  return sixteens == 4 ? launch_decode_q4<D, 1, 8, 4>(prm, st) : launch_decode_q4<D, 1, 8, 2>(prm, st);
 }
 
 jl_status decode_q4(jl::DecodeQ4Params prm, int32_t head_dim, float softmax_scale, void* workspace,

@@ -31,7 +31,7 @@ struct DecodeQ4Params {
   const int32_t* seqlens;
   const float* cos_tab;
   const float* sin_tab;
-  float* ws;                   // o [n_cta][2][heads][D], then (m, l) [n_cta][2][heads][2]
+  float* ws;                   // o [heads of a block][2][n_cta][D], then (m, l) [heads][2][n_cta][2]
   __nv_bfloat16* out;
   float* lse;
   int64_t cache_stride;
@@ -83,12 +83,12 @@ __device__ __forceinline__ int q4_cta_of(int total, int n_cta, int x) {
 
 // Where a range starts: entry and tile inside it.
 struct Q4Start {
-  int hb, b, tile;
+  int hb, b, tile, len;  // head block, entry and its length, tile of the entry
   int begin, end;  // the range in the list of all tiles (the host keeps their number below 2^31)
 };
 
 __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
-  Q4Start s{0, 0, 0, 0, 0};
+  Q4Start s{};
   int t;
   const int all = q4_tiles_before(p, 0, lane, t).x;
   const int total = all * (p.Hkv / p.heads_per_block);
@@ -99,8 +99,8 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
   s.hb = s.begin / all;
   int left = s.begin % all;
   for (int e0 = 0; e0 < p.B; e0 += 32) {
-    const int e = e0 + lane;
-    if (e0 > 0) t = e < p.B ? q4_tiles(p, p.seqlens[e]) : 0;
+    const int e = e0 + lane, len = e < p.B ? p.seqlens[e] : 0;
+    if (e0 > 0) t = q4_tiles(p, len);
     int sum = t;  // inclusive prefix over the lanes
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -112,6 +112,7 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
       const int src = __ffs(here) - 1;
       s.b = e0 + src;
       s.tile = left - __shfl_sync(0xffffffffu, sum - t, src);
+      s.len = __shfl_sync(0xffffffffu, len, src);
       return s;
     }
     left -= __shfl_sync(0xffffffffu, sum, 31);
@@ -150,11 +151,8 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 //
 // The rotations' cos and sin are the same for all heads, so four warps make them once a tile
 // for the whole head block: from the table's row of the tile's first key by steps of one
-// position in fp32 (at most 32 steps), stored as fp16 in the order of the fragments.
+// position in fp32, stored as fp16 in the order of the fragments.
 
-#ifndef Q4_U
-#define Q4_U 2
-#endif
 constexpr int kDecodeQ4Ctas = 148;  // one per SM
 constexpr int kDecodeQ4TabWarps = 3, kDecodeQ4OtherWarps = 1 + kDecodeQ4TabWarps;  // one loads
 constexpr int kDecodeQ4MaxStages = 6;
@@ -288,7 +286,7 @@ __device__ __forceinline__ int q4_turn_at(int key, int w, int t) {
   return key * 2 * D + ((w * 64 + t * 16) ^ ((key & 1) << 6));  // neighbouring rows on different banks
 }
 
-template <int D, int NQ, int KEYS>
+template <int D, int NQ, int KEYS, int U>
 __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
     jl_decode_q4_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                         const __grid_constant__ CUtensorMap ts, const DecodeQ4Params p) {
@@ -299,7 +297,6 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
   constexpr int NP = (NQ + 1) / 2;  // value tiles of eight columns
   constexpr int kF = NQ == 1 ? 2 : 4;  // weight fragments: pairs of scale groups, or groups
   constexpr bool kQueryRegs = NQ <= 2;  // query fragments stay in registers
-  constexpr int U = NQ == 1 ? Q4_U : 1;    // sixteens of keys that a warp takes at once
   extern __shared__ uint8_t raw_smem[];
   __shared__ DecodeQ4Shared sh;
   uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
@@ -327,20 +324,16 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
     Q4Start s = q4_range(p, lane);
     if (__any_sync(0xffffffffu, failed)) s.end = s.begin;
     if (lane == 0) sh.start = s;
-    if (s.begin < s.end) {
-      // The first segment's query and the tables' row for it are asked for before the loads of
-      // the tiles, behind which they would queue for some microseconds.
-      const char* q = reinterpret_cast<const char*>(p.q + (static_cast<int64_t>(s.b) * p.Hq + s.hb * HPB * p.group) * D);
-      for (int x = lane * 128; x < HPB * p.group * D * 2; x += 32 * 128) prefetch_l2(q + x);
-      const int i = p.seqlens[s.b] - 1, nq = i - i / max(1, (i + p.w_pre) / p.w_pre);
-      if (lane < 2 * HALF * 4 / 128)
-        prefetch_l2((lane & 1 ? p.sin_tab : p.cos_tab) + static_cast<int64_t>(nq) * HALF + (lane >> 1) * 32);
-    }
+  } else if (warp == 1) {
+    // The queries of a small batch are asked for before the loads of the tiles, behind which
+    // they would queue for some microseconds.
+    const int bytes = p.B <= 16 ? min(p.B * p.Hq * D * 2, 16384) : 0;
+    for (int x = lane * 128; x < bytes; x += 32 * 128) prefetch_l2(reinterpret_cast<const char*>(p.q) + x);
   }
   __syncthreads();
   const Q4Start st = sh.start;
   int cur = st.begin;
-  int hb = st.hb, b = st.b, t0 = st.tile;
+  int hb = st.hb, b = st.b, t0 = st.tile, L = st.len;
   int stage = 0;
   uint32_t phase = 0;
 
@@ -352,7 +345,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
       const int boxes = T / 16, rows = HPB * HALF / q4_code_row(D, HPB);  // of a tile; of codes, a key
       int issued = 0;
       while (cur < st.end && ok) {
-        const int L = p.seqlens[b], tiles = q4_tiles(p, L);
+        const int tiles = q4_tiles(p, L);
         const int t1 = min(tiles, t0 + (st.end - cur));
         int row = 0;  // lane x: the cache row of box x of the 32 asked for last
         for (int tile = t0; tile < t1; ++tile) {
@@ -393,6 +386,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
           b = 0;
           ++hb;
         }
+        if (cur < st.end) L = p.seqlens[b];
       }
       if (!ok && lane == 0) {
         // gave up: the copies in flight land before the block leaves its shared memory
@@ -402,9 +396,11 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
       return;
     }
     // ------------------------------------------------------------ cos/sin rows --
-    // Eight keys at a time, the warps in turn; each eight starts from the tables' row of its
-    // first key (row j - floor(j / G)) and steps on.  That row is asked for one eight ahead,
-    // after it was brought into L2 some tiles ahead.
+    // Each warp makes a third of a tile's rows: from the tables' row of its first key (row
+    // j - floor(j / G)), asked for a tile ahead, by one position's step after the other in fp32
+    // (at most 88 steps: an error of some 2^-17 before the rounding to fp16).  Eight keys at a
+    // time, each from a row of its own asked for eight keys ahead, took 27 us for 128K keys, the
+    // rows' latency; one warp for all of a tile's rows took 43.
     const int tw = warp - KEYS - 1;
     // lane -> the two pairs of one packed register: word w, fragment lane t, register half e
     const bool has = D == 128 || lane < 16;
@@ -416,60 +412,57 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
     const uint64_t step_c = f2_pack(p.cos_tab[one + c0], p.cos_tab[one + c1]);
     const uint64_t step_s = f2_pack(p.sin_tab[one + c0], p.sin_tab[one + c1]);
     const uint64_t step_n = f2_pack(-p.sin_tab[one + c0], -p.sin_tab[one + c1]);
+    const int row0 = T / 8 * tw / kDecodeQ4TabWarps * 8, row1 = T / 8 * (tw + 1) / kDecodeQ4TabWarps * 8;
     while (cur < st.end && ok) {
-      const int L = p.seqlens[b], tiles = q4_tiles(p, L);
+      const int tiles = q4_tiles(p, L);
       const int t1 = min(tiles, t0 + (st.end - cur));
       const int grow = max(1, (L + p.w_pre - 1) / p.w_pre);
       const int jb = grow > 1 ? L - 1 - p.w0 : -1;  // remote keys are j <= jb
       const int far_tiles = jb < 0 ? 0 : min(t1, jb / T + 1);
-      const int ahead = 4 * T - 4 * T / grow;  // rows that four tiles on begins further, or one more
       float2 next_c = make_float2(1.f, 1.f), next_s = make_float2(0.f, 0.f);
       int next_left = grow;
-      auto ask = [&](int j) {  // keys behind the length may have no row
+      auto ask = [&](int j) {
         const int quot = j / grow;
         next_left = grow - (j - quot * grow);  // keys until f steps; that key keeps the angle of the one before it
-        const int64_t row = min(static_cast<int64_t>(j - quot), p.n_tab_rows - 1) * HALF;
+        const int64_t row = min(static_cast<int64_t>(j - quot), p.n_tab_rows - 1) * HALF;  // behind the length: none
         next_c = make_float2(p.cos_tab[row + c0], p.cos_tab[row + c1]);
         next_s = make_float2(p.sin_tab[row + c0], p.sin_tab[row + c1]);
-        const int64_t later = min(static_cast<int64_t>(j - quot) + ahead, p.n_tab_rows - 1) * HALF;
-        prefetch_l2(p.cos_tab + later + c0);
-        prefetch_l2(p.sin_tab + later + c0);
       };
-      if (t0 < far_tiles) ask(t0 * T + 8 * tw);
+      if (t0 < far_tiles) ask(t0 * T + row0);
       for (int tile = t0; tile < t1; ++tile) {
         if (!warp_wait(&sh.empty[stage], phase ^ 1, abort)) {
           ok = false;
           break;
         }
         if (tile < far_tiles) {
-          uint8_t* const rows = stages + stage * lay.stage + 2 * lay.codes + lay.scales;
-          for (int r = 8 * tw; r < T; r += 8 * kDecodeQ4TabWarps) {
-            uint64_t ac = f2_pack(next_c.x, next_c.y), as = f2_pack(next_s.x, next_s.y);
-            int left = next_left;
-            const int r_next = r + 8 * kDecodeQ4TabWarps;
-            if (r_next < T) ask(tile * T + r_next);
-            else if (tile + 1 < far_tiles) ask((tile + 1) * T + 8 * tw);
-            // even and odd rows from two places, so that the offsets are constants
-            uint8_t* even = rows + q4_turn_at<D>(r, w, t) + 4 * e;
-            uint8_t* odd = rows + q4_turn_at<D>(r + 1, w, t) + 4 * e - 2 * D;
-            if (has) {
+          uint64_t ac = f2_pack(next_c.x, next_c.y), as = f2_pack(next_s.x, next_s.y);
+          int left = next_left;
+          if (tile + 1 < far_tiles) ask((tile + 1) * T + row0);
+          // even and odd rows from two places, so that the offsets in the loop are constants
+          uint8_t* const rows = stages + stage * lay.stage + 2 * lay.codes + lay.scales + row0 * 2 * D;
+          uint8_t* even = rows + q4_turn_at<D>(0, w, t) + 4 * e;
+          uint8_t* odd = rows + q4_turn_at<D>(1, w, t) + 4 * e - 2 * D;
+          for (int r = row0; r < row1; r += 8) {
 #pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                uint8_t* at = (x & 1 ? odd : even) + x * 2 * D;
-                float c[2], sn[2];
-                f2_unpack(ac, c[0], c[1]);
-                f2_unpack(as, sn[0], sn[1]);
+            for (int x = 0; x < 8; ++x) {
+              uint8_t* at = (x & 1 ? odd : even) + x * 2 * D;
+              float c[2], sn[2];
+              f2_unpack(ac, c[0], c[1]);
+              f2_unpack(as, sn[0], sn[1]);
+              if (has) {
                 *reinterpret_cast<__half2*>(at) = __floats2half2_rn(c[0], c[1]);
                 *reinterpret_cast<__half2*>(at + 8) = __floats2half2_rn(sn[0], sn[1]);
-                if (--left == 0) {
-                  left = grow;
-                } else {
-                  const uint64_t nc = f2_fma(ac, step_c, f2_mul(as, step_n));
-                  as = f2_fma(as, step_c, f2_mul(ac, step_s));
-                  ac = nc;
-                }
+              }
+              if (--left == 0) {
+                left = grow;
+              } else {
+                const uint64_t nc = f2_fma(ac, step_c, f2_mul(as, step_n));
+                as = f2_fma(as, step_c, f2_mul(ac, step_s));
+                ac = nc;
               }
             }
+            even += 16 * D;
+            odd += 16 * D;
           }
         }
         __syncwarp();
@@ -485,6 +478,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
         b = 0;
         ++hb;
       }
+      if (cur < st.end) L = p.seqlens[b];
     }
     return;
   }
@@ -513,7 +507,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
   bool ok = true;
 
   while (cur < st.end) {
-    const int L = p.seqlens[b], tiles = q4_tiles(p, L);
+    const int tiles = q4_tiles(p, L);
     const int t1 = min(tiles, t0 + (st.end - cur));
     if (t1 > t0) {
       const int i = L - 1, grow = max(1, (L + p.w_pre - 1) / p.w_pre);
@@ -543,18 +537,22 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
         float cs[2], sn[2];
         cs[0] = p.cos_tab[static_cast<int64_t>(nq) * HALF + c0], cs[1] = p.cos_tab[static_cast<int64_t>(nq) * HALF + c1];
         sn[0] = p.sin_tab[static_cast<int64_t>(nq) * HALF + c0], sn[1] = p.sin_tab[static_cast<int64_t>(nq) * HALF + c1];
+        float top[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+          top[u] = fmaxf(fmaxf(fabsf(y[u][0]), fabsf(y[u][1])), fmaxf(fabsf(y[u][2]), fabsf(y[u][3])));
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+#pragma unroll
+          for (int u = 0; u < kRows; ++u) top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
           const int x = warp + u * KEYS, h = x / (4 * NQ), qh = x % (4 * NQ);
-          if (h >= HPB) break;
-          float top = fmaxf(fmaxf(fabsf(y[u][0]), fabsf(y[u][1])), fmaxf(fabsf(y[u][2]), fabsf(y[u][3])));
-#pragma unroll
-          for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           // 2^up brings the largest channel into [8, 16); up in [-120, 120] keeps both factors normal
-          const int up = min(120, max(-120, 130 - static_cast<int>(__float_as_uint(top) >> 23)));
+          const int up = min(120, max(-120, 130 - static_cast<int>(__float_as_uint(top[u]) >> 23)));
           const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-          if (lane == 0) sh.mul[x] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-          if (has) {
+          if (lane == 0 && h < HPB) sh.mul[x] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+          if (has && h < HPB) {
 #pragma unroll
             for (int var = 0; var < 2; ++var) {
               uint32_t* at = reinterpret_cast<uint32_t*>(smem) + (((var * HPB + h) * NQ + qh / 4) * KW + w) * 128;
@@ -843,7 +841,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
         for (int x = 4; x < 32; x <<= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], x);
       const bool whole = t0 == 0 && t1 == tiles;
       const int hpb = HPB * p.group;
-      const int64_t slot0 = (static_cast<int64_t>(blockIdx.x) * 2 + (cur == st.begin ? 0 : 1)) * hpb;
+      const int slot0 = (cur == st.begin ? 0 : p.n_cta) + blockIdx.x;  // query head q's partial: slot0 + 2 q n_cta
       float* ml = p.ws + static_cast<int64_t>(p.n_cta) * 2 * hpb * D;
       if (wph == 1) {  // this warp has all of its head: straight from its registers
 #pragma unroll
@@ -851,6 +849,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
           if (4 * n + t >= p.group) continue;
           const int q = head * p.group + 4 * n + t;
           const int64_t at = static_cast<int64_t>(b) * p.Hq + hb * hpb + q;
+          const int slot = slot0 + 2 * q * p.n_cta;
           const float inv = 1.f / l[n];
 #pragma unroll
           for (int x = 0; x < MT; ++x) {
@@ -861,12 +860,12 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
               p.out[at * D + 16 * x + g] = __float2bfloat16_rn(lo * inv);
               p.out[at * D + 16 * x + 8 + g] = __float2bfloat16_rn(hi * inv);
             } else {
-              p.ws[(slot0 + q) * D + 16 * x + g] = lo;
-              p.ws[(slot0 + q) * D + 16 * x + 8 + g] = hi;
+              p.ws[static_cast<int64_t>(slot) * D + 16 * x + g] = lo;
+              p.ws[static_cast<int64_t>(slot) * D + 16 * x + 8 + g] = hi;
             }
           }
           if (g == 0) {
-            if (!whole) *reinterpret_cast<float2*>(ml + (slot0 + q) * 2) = make_float2(m[n], l[n]);
+            if (!whole) *reinterpret_cast<float2*>(ml + slot * 2) = make_float2(m[n], l[n]);
             else if (p.lse != nullptr) p.lse[at] = (m[n] + log2f(l[n])) * 0.69314718055994531f;
           }
         }
@@ -914,8 +913,9 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
               make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
           if (c == 0 && p.lse != nullptr) p.lse[at] = (mx + log2f(lsum)) * 0.69314718055994531f;
         } else {
-          *reinterpret_cast<float4*>(p.ws + (slot0 + q) * D + c) = acc;
-          if (c == 0) *reinterpret_cast<float2*>(ml + (slot0 + q) * 2) = make_float2(mx, lsum);
+          const int slot = slot0 + 2 * q * p.n_cta;
+          *reinterpret_cast<float4*>(p.ws + static_cast<int64_t>(slot) * D + c) = acc;
+          if (c == 0) *reinterpret_cast<float2*>(ml + slot * 2) = make_float2(mx, lsum);
         }
       }
       }
@@ -927,6 +927,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
       b = 0;
       ++hb;
     }
+    if (cur < st.end) L = p.seqlens[b];
   }
 }
 
@@ -934,17 +935,18 @@ constexpr int kCombineQ4Threads = 256;
 
 // Joins the partials of one (entry, query head), which lie in the ranges of CTAs c0 .. c1;
 // writes zeros and -inf for an empty entry, NaN for a length outside the contract (reported
-// by jl_sync_status) or a kernel that gave up.  Every thread asks for what it needs before it
-// waits for any of it: thread c for the maximum and sum of partial c0 + c, and the channels
-// of its first partials.  SPLIT blocks share a head, each a part of its channels: with few
-// heads to join, one block a head left 32 SMs to fetch 77 KB each (3.2 us against 0.9).
+// by jl_sync_status) or a kernel that gave up.  SPLIT blocks share a head, each a part of its
+// channels: with few heads to join, one block a head left 32 SMs to fetch 77 KB each (3.2 us
+// against 0.9).  Every warp asks at once for the maxima and sums of all partials, which it
+// needs for its weights, and for its channels of the first ones: one round trip and one
+// barrier for up to 148 partials.
 template <int D, int SPLIT>
 __global__ void __launch_bounds__(kCombineQ4Threads) jl_decode_q4_combine_kernel(const DecodeQ4Params p) {
   constexpr int NW = kCombineQ4Threads / 32, CH = D / SPLIT, LANES = CH / 4;  // a float4 a lane
   constexpr int ROWS = kCombineQ4Threads / LANES, PER = 5;                    // partials at a time, and rounds in flight
-  static_assert(kDecodeQ4Ctas <= kCombineQ4Threads, "a thread for each partial");
-  __shared__ float weight[kCombineQ4Threads], red[2][NW];
-  __shared__ __align__(16) float sum[ROWS][CH];
+  constexpr int OWN = (kDecodeQ4Ctas + 31) / 32;
+  __shared__ float weight[NW][32 * OWN];
+  __shared__ __align__(16) float sum[NW][CH];
   const int qh = blockIdx.x / SPLIT, ch = blockIdx.x % SPLIT * CH + threadIdx.x % LANES * 4, row = threadIdx.x / LANES;
   const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_launch_dependents();
@@ -959,65 +961,72 @@ __global__ void __launch_bounds__(kCombineQ4Threads) jl_decode_q4_combine_kernel
   const int c0 = t ? q4_cta_of(total, n_cta, first) : 0, c1 = t ? q4_cta_of(total, n_cta, first + t - 1) : 0;
   const int s0 = t && q4_range_begin(total, n_cta, c0) == first ? 0 : 1;
   const int count = c1 > c0 ? c1 - c0 + 1 : 0;  // 0: the decode wrote the result, or there is none
-  auto slot = [&](int c) { return ((c0 + c) * 2LL + (c == 0 ? s0 : 0)) * hpb + qh % hpb; };
+  // the partials of a head lie side by side: by CTA, first those of segments that begin a range
+  auto slot = [&](int c) { return (2 * (qh % hpb) + (c == 0 ? s0 : 0)) * p.n_cta + c0 + c; };
   const float* ml = p.ws + static_cast<int64_t>(p.n_cta) * 2 * hpb * D;
-  griddep_wait();
   const bool wrong = L < 0 || L > p.max_seqlen;
+  griddep_wait();
   const bool bad = wrong || status_failed();
-  float2 own = make_float2(-INFINITY, 0.f);
-  if (threadIdx.x < count) own = *reinterpret_cast<const float2*>(ml + slot(threadIdx.x) * 2);
+  float2 own[OWN];  // maxima and sums, lane + 32 x
+#pragma unroll
+  for (int x = 0; x < OWN; ++x)
+    own[x] = lane + 32 * x < count ? *reinterpret_cast<const float2*>(ml + slot(lane + 32 * x) * 2)
+                                   : make_float2(-INFINITY, 0.f);
   float4 o[PER];
   auto ask = [&](int c) {
 #pragma unroll
     for (int u = 0; u < PER; ++u)
-      if (c + u * ROWS < count) o[u] = *reinterpret_cast<const float4*>(p.ws + slot(c + u * ROWS) * D + ch);
+      if (c + u * ROWS < count) o[u] = *reinterpret_cast<const float4*>(p.ws + static_cast<int64_t>(slot(c + u * ROWS)) * D + ch);
   };
   ask(row);
   const int64_t at = static_cast<int64_t>(b) * p.Hq + qh;
-  if (__syncthreads_or(bad) || t == 0) {
-    if (wrong && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(&g_status, kDevErrBounds);
-    const bool nan = bad || t != 0;
-    const float x = nan ? __int_as_float(0x7fc00000) : 0.f;
+  if (bad || t == 0) {  // the same for all threads: nothing sets the status word meanwhile but this
+    const float x = bad ? __int_as_float(0x7fc00000) : 0.f;
     if (row == 0) *reinterpret_cast<uint2*>(p.out + at * D + ch) = make_uint2(pack_bf16x2(x, x), pack_bf16x2(x, x));
-    if (threadIdx.x == 0 && blockIdx.x % SPLIT == 0 && p.lse != nullptr) p.lse[at] = nan ? x : -INFINITY;
+    if (threadIdx.x == 0 && blockIdx.x % SPLIT == 0) {
+      if (p.lse != nullptr) p.lse[at] = bad ? x : -INFINITY;
+      if (wrong && qh == 0) atomicOr(&g_status, kDevErrBounds);
+    }
     return;
   }
   if (count == 0) return;
-  float mx = own.x;
+  float mx = own[0].x;
+#pragma unroll
+  for (int x = 1; x < OWN; ++x) mx = fmaxf(mx, own[x].x);
 #pragma unroll
   for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-  if (lane == 0) red[0][warp] = mx;
-  __syncthreads();
-  mx = red[0][0];
+  float l = 0.f;
 #pragma unroll
-  for (int w = 1; w < NW; ++w) mx = fmaxf(mx, red[0][w]);
-  const float f = own.x == -INFINITY ? 1.f : ex2_approx(own.x - mx);  // -inf: the sum is 0, or the NaN of NaN scores
-  weight[threadIdx.x] = f;
-  float l = own.y * f;
+  for (int x = 0; x < OWN; ++x) {
+    const float f = own[x].x == -INFINITY ? 1.f : ex2_approx(own[x].x - mx);  // -inf: l is 0, or the NaN of NaN scores
+    weight[warp][lane + 32 * x] = f;
+    l = fmaf(own[x].y, f, l);
+  }
 #pragma unroll
   for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-  if (lane == 0) red[1][warp] = l;
-  __syncthreads();
+  __syncwarp();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int c = row; c < count; c += PER * ROWS) {
     if (c != row) ask(c);
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
       if (c + u * ROWS >= count) break;
-      const float w = weight[c + u * ROWS];
+      const float w = weight[warp][c + u * ROWS];
       acc.x = fmaf(o[u].x, w, acc.x), acc.y = fmaf(o[u].y, w, acc.y);
       acc.z = fmaf(o[u].z, w, acc.z), acc.w = fmaf(o[u].w, w, acc.w);
     }
   }
-  *reinterpret_cast<float4*>(&sum[row][threadIdx.x % LANES * 4]) = acc;
-  __syncthreads();
-  l = 0.f;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) l += red[1][w];
+  for (int x = LANES; x < 32; x <<= 1) {  // the warp's rows
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, x), acc.y += __shfl_xor_sync(0xffffffffu, acc.y, x);
+    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, x), acc.w += __shfl_xor_sync(0xffffffffu, acc.w, x);
+  }
+  if (lane < LANES) *reinterpret_cast<float4*>(&sum[warp][lane * 4]) = acc;
+  __syncthreads();
   if (threadIdx.x < CH) {
     float x = 0.f;
-#pragma unroll 8
-    for (int r = 0; r < min(ROWS, count); ++r) x += sum[r][threadIdx.x];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) x += sum[w][threadIdx.x];
     p.out[at * D + blockIdx.x % SPLIT * CH + threadIdx.x] = __float2bfloat16_rn(x / l);
   }
   if (threadIdx.x == 0 && blockIdx.x % SPLIT == 0 && p.lse != nullptr)

@@ -441,9 +441,10 @@ def test_two_captured_graphs_share_a_workspace_in_turn(jl):
             close(out, None, want)
 
 
-def test_a_long_cache(jl):
-    """G = 3 at 70001 keys, offsets behind 2^31 bits in the codes, lse to fp32's accuracy."""
-    d, hq, hkv, L = 128, 16, 4, 70001
+@pytest.mark.parametrize("d,hq,hkv", [(128, 16, 4), (128, 32, 8), (64, 8, 8), (128, 4, 1), (128, 16, 2), (128, 20, 2)])
+def test_a_long_cache(jl, d, hq, hkv):
+    """G = 3 at 70001 keys: many tiles to a CTA, offsets behind 2^31 bits in the codes, lse to fp32's accuracy."""
+    L = 70001
     cache = random_cache(43, 1, L, hkv, d)
     q = normal(44, 1, hq, d)
     cos, sin = tables(L, d)
