@@ -160,14 +160,18 @@ __device__ __forceinline__ void q4_write_row(const Q4Params& p, bool live, const
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < NP / 2; ++i) {
-    const uint64_t c = f2_pack(cs[2 * i], cs[2 * i + 1]), s = f2_pack(sn[2 * i], sn[2 * i + 1]);
+    // packed products, but scalar sums: a packed sum of packed products was found to be fused
+    const uint64_t c = f2_pack(cs[2 * i], cs[2 * i + 1]), z = f2_pack(sn[2 * i], sn[2 * i + 1]);
     const uint64_t a = f2_pack(__uint_as_float(ka[i] << 16), __uint_as_float(ka[i] & 0xffff0000u));
     const uint64_t b = f2_pack(__uint_as_float(kb[i] << 16), __uint_as_float(kb[i] & 0xffff0000u));
-    ya[i] = f2_sub(f2_mul(a, c), f2_mul(b, s));
-    yb[i] = f2_add(f2_mul(b, c), f2_mul(a, s));
-    float x0, x1, x2, x3;
-    f2_unpack(ya[i], x0, x1);
-    f2_unpack(yb[i], x2, x3);
+    float ac0, ac1, as0, as1, bc0, bc1, bs0, bs1;
+    f2_unpack(f2_mul(a, c), ac0, ac1);
+    f2_unpack(f2_mul(a, z), as0, as1);
+    f2_unpack(f2_mul(b, c), bc0, bc1);
+    f2_unpack(f2_mul(b, z), bs0, bs1);
+    const float x0 = __fsub_rn(ac0, bs0), x1 = __fsub_rn(ac1, bs1), x2 = __fadd_rn(bc0, as0), x3 = __fadd_rn(bc1, as1);
+    ya[i] = f2_pack(x0, x1);
+    yb[i] = f2_pack(x2, x3);
     top = max_nan(max_nan(max_nan(fabsf(x0), fabsf(x1)), max_nan(fabsf(x2), fabsf(x3))), top);
   }
   __nv_bfloat162 vtop = __habs2(*reinterpret_cast<__nv_bfloat162*>(&vv[0]));
@@ -257,7 +261,7 @@ __device__ __forceinline__ int64_t q4_split(int64_t row, int Hkv, int& h) {
 
 // Prompt tokens: token t of sequence b goes to position past[b] + t - cu_seqlens[b].
 template <int D>
-__global__ void __launch_bounds__(4 * kQ4Teams) jl_kv_fill_q4_kernel(const Q4Params p) {
+__global__ void __launch_bounds__(4 * kQ4Teams, 3) jl_kv_fill_q4_kernel(const Q4Params p) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kQ4Teams + threadIdx.x / 4;
   const int w = threadIdx.x & 3;
   bool live = row < p.total_tokens * p.Hkv;

@@ -113,6 +113,22 @@ def test_fill_writes_the_reference_codes(jl, d, hkv, lens, past, page):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_have_the_reference_codes(jl, d):
+    """Roundings that depend on the order of a key's products and sums show in some ten groups of four
+    million: a rotation whose products are fused into its sums is not the one that the codes are defined by."""
+    T, hkv = 40000, 8
+    k, v = normal(61, T, hkv, d), normal(62, T, hkv, d)
+    cos, sin = tables(T, d)
+    cache = jl.jl_kv_cache_q4_empty(1, T, hkv, d)
+    jl.jl_kv_cache_fill_q4(k, v, dev([0, T], torch.int32), cos, sin, *cache)
+    jl.jl_sync_status()
+    c, s = R.tables(T, d, BASE)
+    code, scale = R.quantise(R.rotate_f32(R.f32(k), c[:, None], s[:, None]), R.key_group)
+    assert np.array_equal(R.f32(cache[2][0, :, :, :4]), scale)
+    assert np.array_equal(R.codes(cache[0][0].cpu().numpy(), d, R.key_place), code)
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_groups_of_zeros_extremes_and_nonfinite_values(jl, d):
     x = normal(3, 12, 1, d).float()
     x[0] = 0
