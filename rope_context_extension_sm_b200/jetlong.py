@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -466,7 +467,7 @@ def jl_kv_cache_q4_empty(n: int, stride: int, n_kv_heads: int, head_dim: int, *,
 # The checks below run for every token that a serving loop decodes, so each tensor is checked in one
 # expression, and only a failed one is looked at again for its message.
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _q4_bad(t, dtype, shape, dev, name):
@@ -479,9 +480,9 @@ def _q4_bad(t, dtype, shape, dev, name):
 
 def _q4_is(t, dtype, shape, dev, name) -> int:
     """Checks a tensor and returns its address."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        _q4_bad(t, dtype, shape, dev, name)
-    return t.data_ptr()
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _q4_bad(t, dtype, shape, dev, name)
 
 
 def _q4_cache(k_codes, v_codes, scales, block_table, batch: int):
@@ -522,7 +523,7 @@ def _q4_alloc(stream, dev: int):
 def _q4_call(name: str, stream, dev: int, *args) -> None:
     """Calls the entry point on the tensors' device, on the stream given or that device's current one."""
     raw = _raw_stream(dev) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         status = getattr(_lib, name)(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -596,8 +597,8 @@ def _read_q4(name, k_codes, v_codes, scales, lens, starts, k_out, v_out, rows, s
     shape = (B, rows, hkv, d)
     if k_out is None or v_out is None:
         with contextlib.nullcontext() if stream is None else _q4_alloc(stream, dev):
-            k_out = torch.empty(shape, dtype=_BF16, device=k_codes.device) if k_out is None else k_out
-            v_out = torch.empty(shape, dtype=_BF16, device=k_codes.device) if v_out is None else v_out
+            k_out = scales.new_empty(shape) if k_out is None else k_out
+            v_out = scales.new_empty(shape) if v_out is None else v_out
     _q4_call(name, stream, dev, *cache, *where,
              None if starts is None else _q4_is(starts, _I32, (B,), dev, "starts"),
              _q4_is(lens, _I32, (B,), dev, "lens"), B, hkv, d, _q4_is(k_out, _BF16, shape, dev, "k_out"),
@@ -621,7 +622,22 @@ def jl_kv_cache_read_q4_paged(k_codes, v_codes, scales, block_table, lens, *, st
 
 
 def jl_bifocal_decode_q4_workspace_size(Hq: int, head_dim: int) -> int:
-    return int(_lib.jl_bifocal_decode_q4_workspace_size(Hq, head_dim))
+    return _decode_q4_workspace(Hq, head_dim)
+
+
+@functools.lru_cache(maxsize=None)
+def _decode_q4_workspace(hq: int, d: int) -> int:
+    return int(_lib.jl_bifocal_decode_q4_workspace_size(hq, d))
+
+
+def _decode_q4_outputs(q, B, hq, d, out, lse, workspace, want_lse):
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = q.new_empty((B, hq), dtype=_F32)
+    if workspace is None:
+        workspace = q.new_empty(_decode_q4_workspace(hq, d), dtype=_U8)
+    return out, lse, workspace
 
 
 def _decode_q4(name, q, k_codes, v_codes, scales, seqlens, max_seqlen, w0, w_pretrained, cos, sin, softmax_scale, out,
@@ -631,14 +647,11 @@ def _decode_q4(name, q, k_codes, v_codes, scales, seqlens, max_seqlen, w0, w_pre
         _need(q, _BF16, "q", 3)
     B, hq = shape[:2]
     dev, hkv, d, cache, where = _q4_cache(k_codes, v_codes, scales, block_table, B)
-    if out is None or workspace is None or (lse is None and want_lse):
-        with contextlib.nullcontext() if stream is None else _q4_alloc(stream, dev):
-            if out is None:
-                out = torch.empty_like(q)
-            if lse is None and want_lse:
-                lse = torch.empty((B, hq), dtype=_F32, device=q.device)
-            if workspace is None:
-                workspace = torch.empty(_lib.jl_bifocal_decode_q4_workspace_size(hq, d), dtype=_U8, device=q.device)
+    if stream is None:
+        out, lse, workspace = _decode_q4_outputs(q, B, hq, d, out, lse, workspace, want_lse)
+    else:
+        with _q4_alloc(stream, dev):
+            out, lse, workspace = _decode_q4_outputs(q, B, hq, d, out, lse, workspace, want_lse)
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the cache's device")
     lens = _q4_is(seqlens, _I32, (B,), dev, "seqlens")
