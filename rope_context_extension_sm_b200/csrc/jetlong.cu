@@ -740,7 +740,8 @@ jl_status launch_decode_q4(const jl::DecodeQ4Params& prm, cudaStream_t st) {
   // Four blocks a head while that leaves room on the SMs (148 of four or more blocks each).
   const bool split = static_cast<int64_t>(prm.Hq) * prm.B * 4 <= 1024;
   e = launch_pdl(split ? jl::jl_decode_q4_combine_kernel<D, 4> : jl::jl_decode_q4_combine_kernel<D, 1>,
-                 dim3(prm.Hq * (split ? 4 : 1), prm.B), dim3(jl::kCombineQ4Threads), 0, st, prm);
+                 dim3(prm.heads_per_block * prm.group * (split ? 4 : 1), prm.B, prm.Hkv / prm.heads_per_block),
+                 dim3(jl::kCombineQ4Threads), 0, st, prm);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit decode combine launch");
   return ok();
 }
@@ -755,6 +756,7 @@ jl_status dispatch_decode_q4(jl::DecodeQ4Params& prm, cudaStream_t st) {
   const int sixteens = nq > 1 ? 1 : hpb == 8 ? 4 : 2;
   prm.heads_per_block = hpb;
   prm.tile = 16 * sixteens * 8 / hpb;
+  prm.tile_log2 = __builtin_ctz(prm.tile);
   const int64_t tiles = (static_cast<int64_t>(prm.max_seqlen) + prm.tile - 1) / prm.tile * prm.B * (prm.Hkv / hpb);
   if (tiles > 0x7fffffff) return fail(JL_ERR_UNSUPPORTED, "too many keys for one call (%lld tiles)", (long long)tiles);
   prm.n_cta = static_cast<int32_t>(std::min<int64_t>(jl::kDecodeQ4Ctas, tiles));
@@ -795,7 +797,8 @@ jl_status decode_q4(jl::DecodeQ4Params prm, int32_t head_dim, float softmax_scal
                 prm.max_seqlen);
   if (!paged && prm.B * prm.cache_stride > 0x7fffffffLL)
     return fail(JL_ERR_UNSUPPORTED, "B * cache_stride must be < 2^31 (got %lld)", (long long)(prm.B * prm.cache_stride));
-  if (prm.B > 65535) return fail(JL_ERR_UNSUPPORTED, "B must be <= 65535 (got %d)", prm.B);
+  if (prm.B > 65535 || prm.Hkv > 65535)  // dimensions of the combine's grid
+    return fail(JL_ERR_UNSUPPORTED, "B and Hkv must be <= 65535 (got %d, %d)", prm.B, prm.Hkv);
   if (!prm.q || !prm.k_codes || !prm.v_codes || !prm.scales || !prm.seqlens || !prm.cos_tab || !prm.sin_tab ||
       !prm.out || !workspace || (paged && !prm.block_table))
     return fail(JL_ERR_INVALID, "null pointer argument");

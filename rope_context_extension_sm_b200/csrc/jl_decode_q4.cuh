@@ -42,14 +42,14 @@ struct DecodeQ4Params {
   int32_t w0, w_pre, max_seqlen;
   int32_t n_cta;
   int32_t heads_per_block;     // KV heads of a head block
-  int32_t tile;                // keys of a tile
+  int32_t tile, tile_log2;     // keys of a tile, a power of two
   float scale_log2;
 };
 
 // Tiles of an entry of length L (0 for an empty one, or for a length outside the contract,
 // which the combine reports).
 __device__ __forceinline__ int q4_tiles(const DecodeQ4Params& p, int L) {
-  return L < 1 || L > p.max_seqlen ? 0 : (L + p.tile - 1) / p.tile;
+  return L < 1 || L > p.max_seqlen ? 0 : ((L - 1) >> p.tile_log2) + 1;
 }
 
 // Tiles of all entries, and of the entries before b, by one warp; `first` is the tiles of
@@ -70,15 +70,9 @@ __device__ __forceinline__ int2 q4_tiles_before(const DecodeQ4Params& p, int b, 
   return make_int2(all, before);
 }
 
-// CTAs that get a range (every one of at least a tile), the first tile of CTA c's range, and
-// the CTA that holds tile x.
-__device__ __forceinline__ int q4_ctas(const DecodeQ4Params& p, int total) { return min(p.n_cta, total); }
-__device__ __forceinline__ int q4_range_begin(int total, int n_cta, int c) {  // floor(total c / n_cta)
-  const unsigned q = static_cast<unsigned>(total) / n_cta, r = static_cast<unsigned>(total) % n_cta;
-  return q * c + r * static_cast<unsigned>(c) / n_cta;
-}
-__device__ __forceinline__ int q4_cta_of(int total, int n_cta, int x) {
-  return static_cast<int>(((x + 1LL) * n_cta - 1) / total);
+// Tiles of a CTA's range: CTA c has tiles [c per, (c + 1) per) of the list.
+__device__ __forceinline__ int q4_per_cta(const DecodeQ4Params& p, int total) {
+  return (static_cast<unsigned>(total) + p.n_cta - 1) / static_cast<unsigned>(p.n_cta);
 }
 
 // Where a range starts: entry and tile inside it.
@@ -92,10 +86,10 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
   int t;
   const int all = q4_tiles_before(p, 0, lane, t).x;
   const int total = all * (p.Hkv / p.heads_per_block);
-  const int n_cta = q4_ctas(p, total);
-  if (static_cast<int>(blockIdx.x) >= n_cta) return s;
-  s.begin = q4_range_begin(total, n_cta, blockIdx.x);
-  s.end = q4_range_begin(total, n_cta, blockIdx.x + 1);
+  const int per = q4_per_cta(p, total);
+  s.begin = min(static_cast<int64_t>(total), static_cast<int64_t>(per) * blockIdx.x);
+  s.end = min(total, s.begin + per);
+  if (s.begin >= s.end) return s;
   s.hb = s.begin / all;
   int left = s.begin % all;
   for (int e0 = 0; e0 < p.B; e0 += 32) {
@@ -947,22 +941,21 @@ __global__ void __launch_bounds__(kCombineQ4Threads) jl_decode_q4_combine_kernel
   constexpr int OWN = (kDecodeQ4Ctas + 31) / 32;
   __shared__ float weight[NW][32 * OWN];
   __shared__ __align__(16) float sum[NW][CH];
-  const int qh = blockIdx.x / SPLIT, ch = blockIdx.x % SPLIT * CH + threadIdx.x % LANES * 4, row = threadIdx.x / LANES;
+  const int hpb = p.heads_per_block * p.group, hb = blockIdx.z, q = blockIdx.x / SPLIT;  // head block, head in it
+  const int ch = blockIdx.x % SPLIT * CH + threadIdx.x % LANES * 4, row = threadIdx.x / LANES;
   const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_launch_dependents();
   // The decode lets this kernel start only after it waited for everything before it, so the
   // lengths are there; its own partials and the status word are there after the wait.
-  const int hpb = p.heads_per_block * p.group, hb = qh / hpb;
   const int L = p.seqlens[b], t = q4_tiles(p, L);
   int unused;
   const int2 n = q4_tiles_before(p, b, lane, unused);
-  const int total = n.x * (p.Hkv / p.heads_per_block), first = hb * n.x + n.y;
-  const int n_cta = q4_ctas(p, total);
-  const int c0 = t ? q4_cta_of(total, n_cta, first) : 0, c1 = t ? q4_cta_of(total, n_cta, first + t - 1) : 0;
-  const int s0 = t && q4_range_begin(total, n_cta, c0) == first ? 0 : 1;
+  const unsigned per = max(1, q4_per_cta(p, n.x * (p.Hkv / p.heads_per_block))), first = hb * n.x + n.y;
+  const int c0 = first / per, c1 = t ? (first + t - 1) / per : c0;
+  const int s0 = c0 * per == first ? 0 : 1;
   const int count = c1 > c0 ? c1 - c0 + 1 : 0;  // 0: the decode wrote the result, or there is none
   // the partials of a head lie side by side: by CTA, first those of segments that begin a range
-  auto slot = [&](int c) { return (2 * (qh % hpb) + (c == 0 ? s0 : 0)) * p.n_cta + c0 + c; };
+  auto slot = [&](int c) { return (2 * q + (c == 0 ? s0 : 0)) * p.n_cta + c0 + c; };
   const float* ml = p.ws + static_cast<int64_t>(p.n_cta) * 2 * hpb * D;
   const bool wrong = L < 0 || L > p.max_seqlen;
   griddep_wait();
@@ -979,13 +972,13 @@ __global__ void __launch_bounds__(kCombineQ4Threads) jl_decode_q4_combine_kernel
       if (c + u * ROWS < count) o[u] = *reinterpret_cast<const float4*>(p.ws + static_cast<int64_t>(slot(c + u * ROWS)) * D + ch);
   };
   ask(row);
-  const int64_t at = static_cast<int64_t>(b) * p.Hq + qh;
+  const int64_t at = static_cast<int64_t>(b) * p.Hq + hb * hpb + q;
   if (bad || t == 0) {  // the same for all threads: nothing sets the status word meanwhile but this
     const float x = bad ? __int_as_float(0x7fc00000) : 0.f;
     if (row == 0) *reinterpret_cast<uint2*>(p.out + at * D + ch) = make_uint2(pack_bf16x2(x, x), pack_bf16x2(x, x));
     if (threadIdx.x == 0 && blockIdx.x % SPLIT == 0) {
       if (p.lse != nullptr) p.lse[at] = bad ? x : -INFINITY;
-      if (wrong && qh == 0) atomicOr(&g_status, kDevErrBounds);
+      if (wrong && q == 0) atomicOr(&g_status, kDevErrBounds);
     }
     return;
   }
@@ -998,6 +991,7 @@ __global__ void __launch_bounds__(kCombineQ4Threads) jl_decode_q4_combine_kernel
   float l = 0.f;
 #pragma unroll
   for (int x = 0; x < OWN; ++x) {
+    if (32 * x >= count) break;
     const float f = own[x].x == -INFINITY ? 1.f : ex2_approx(own[x].x - mx);  // -inf: l is 0, or the NaN of NaN scores
     weight[warp][lane + 32 * x] = f;
     l = fmaf(own[x].y, f, l);
