@@ -718,7 +718,7 @@ jl_status make_q4_map(CUtensorMap* map, const void* base, int64_t rows, int grou
   return JL_OK;
 }
 
-template <int D, int NQ, int KEYS, int U>
+template <int D, int NQ, int U>
 jl_status launch_decode_q4(const jl::DecodeQ4Params& prm, cudaStream_t st) {
   const int64_t rows = prm.block_table != nullptr ? static_cast<int64_t>(prm.num_pages) * prm.page_size
                                                   : prm.B * prm.cache_stride;
@@ -728,14 +728,14 @@ jl_status launch_decode_q4(const jl::DecodeQ4Params& prm, cudaStream_t st) {
   if ((s = make_q4_map(&tk, prm.k_codes, rows, groups, width, hpb * (D / 2) / width)) != JL_OK) return s;
   if ((s = make_q4_map(&tv, prm.v_codes, rows, groups, width, hpb * (D / 2) / width)) != JL_OK) return s;
   if ((s = make_q4_map(&ts, prm.scales, rows, prm.Hkv / hpb, 16 * hpb, 1)) != JL_OK) return s;
-  const int smem = jl::decode_q4_layout(D, NQ, KEYS, prm.heads_per_block, prm.tile).total;
-  auto kern = jl::jl_decode_q4_kernel<D, NQ, KEYS, U>;
+  const int smem = jl::decode_q4_layout(D, NQ, prm.heads_per_block, prm.tile).total;
+  auto kern = jl::jl_decode_q4_kernel<D, NQ, U>;
   const KernelAttr attr = kernel_attr(reinterpret_cast<const void*>(kern), 222 * 1024);
   if (attr.err != cudaSuccess) return cuda_fail(attr.err, "cudaFuncSetAttribute(4-bit decode)");
-  if (attr.regs < jl::DecodeQ4Warps<KEYS>::kRegs)  // setmaxnreg draws on the launch's registers and would wait for good
+  if (attr.regs < jl::kDecodeQ4Regs)  // setmaxnreg draws on the launch's registers and would wait for good
     return fail(JL_ERR_UNSUPPORTED, "4-bit decode built with %d registers per thread; the register split needs %d",
-                attr.regs, jl::DecodeQ4Warps<KEYS>::kRegs);
-  cudaError_t e = launch_pdl(kern, dim3(prm.n_cta), dim3(jl::DecodeQ4Warps<KEYS>::kThreads), smem, st, tk, tv, ts, prm);
+                attr.regs, jl::kDecodeQ4Regs);
+  cudaError_t e = launch_pdl(kern, dim3(prm.n_cta), dim3(jl::kDecodeQ4Threads), smem, st, tk, tv, ts, prm);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit decode launch");
   // Four blocks a head while that leaves room on the SMs (148 of four or more blocks each).
   const bool split = static_cast<int64_t>(prm.Hq) * prm.B * 4 <= 1024;
@@ -748,8 +748,12 @@ jl_status launch_decode_q4(const jl::DecodeQ4Params& prm, cudaStream_t st) {
 
 template <int D>
 jl_status dispatch_decode_q4(jl::DecodeQ4Params& prm, cudaStream_t st) {
-  // Score tiles of four query heads; KV heads of a block (they share the cos/sin rows); key
-  // warps; keys of a tile: sixteen for each warp of a head, Q4_NB times.
+  // Score tiles of four query heads (two columns each in an n = 8 matrix instruction); KV heads
+  // of a block, which share its cos/sin rows, as many as eight key warps and
+  // 32 KB of query fragments allow; sixteens of keys that a warp takes at once: four chains
+  // hide more latency than two (47.8 against 50.5 us at 128K keys, 32/8 heads), but smaller head
+  // blocks have longer tiles and would be left with one stage in shared memory, and more score
+  // tiles have chains enough and no registers.
   const int nq = prm.group <= 4 ? 1 : prm.group <= 8 ? 2 : 4;
   int hpb = 8 / nq;
   while (prm.Hkv % hpb != 0) hpb /= 2;
@@ -760,9 +764,9 @@ jl_status dispatch_decode_q4(jl::DecodeQ4Params& prm, cudaStream_t st) {
   const int64_t tiles = (static_cast<int64_t>(prm.max_seqlen) + prm.tile - 1) / prm.tile * prm.B * (prm.Hkv / hpb);
   if (tiles > 0x7fffffff) return fail(JL_ERR_UNSUPPORTED, "too many keys for one call (%lld tiles)", (long long)tiles);
   prm.n_cta = static_cast<int32_t>(std::min<int64_t>(jl::kDecodeQ4Ctas, tiles));
-  if (nq == 4) return launch_decode_q4<D, 4, 8, 1>(prm, st);
-  if (nq == 2) return launch_decode_q4<D, 2, 8, 1>(prm, st);
-  return sixteens == 4 ? launch_decode_q4<D, 1, 8, 4>(prm, st) : launch_decode_q4<D, 1, 8, 2>(prm, st);
+  if (nq == 4) return launch_decode_q4<D, 4, 1>(prm, st);
+  if (nq == 2) return launch_decode_q4<D, 2, 1>(prm, st);
+  return sixteens == 4 ? launch_decode_q4<D, 1, 4>(prm, st) : launch_decode_q4<D, 1, 2>(prm, st);
 }
 
 jl_status decode_q4(jl::DecodeQ4Params prm, int32_t head_dim, float softmax_scale, void* workspace,

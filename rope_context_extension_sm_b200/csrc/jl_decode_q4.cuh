@@ -46,6 +46,9 @@ struct DecodeQ4Params {
   float scale_log2;
 };
 
+// G of a length L >= 1.
+__device__ __forceinline__ int q4_group(const DecodeQ4Params& p, int L) { return (L - 1) / p.w_pre + 1; }
+
 // Tiles of an entry of length L (0 for an empty one, or for a length outside the contract,
 // which the combine reports).
 __device__ __forceinline__ int q4_tiles(const DecodeQ4Params& p, int L) {
@@ -116,16 +119,28 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 
 // ------------------------------------------------------------- the decode kernel --
 //
-// Shape.  Eight or sixteen warps of a CTA take keys, four prepare what they need.  A tile is
-// `tile` keys of all KV heads of a head block: sixteen keys for each key warp, of one or two
-// heads.  It arrives by TMA as boxes of sixteen keys, in a ring of stages.
+// What bounds it.  A row of 128 channels is 144 bytes: 128K keys of eight heads are 151 MB,
+// 23.0 us at the measured 6.56 TB/s.  Beside that stand, for 16 keys of one head (8192 of
+// those a head at 128K), some 360 warp instructions to expand, rotate, weigh and sum 4096
+// codes, 40 thousand a scheduler, of which the ALU and the fp16 pipe take two cycles each.
+// Measured (graph-replayed, 32/8 heads of 128, cold caches): 47.8 us at 128K keys (G = 4),
+// 3.2 TB/s, of which 37 us are per key and 10 for the start, the first loads and the join;
+// without rotation (G = 1) 28 us are per key.  8K keys take 10.4 us.  With the instructions
+// of the keys and values left out, the loads alone stream 128K keys in 21 us.  So the
+// arithmetic bounds it: issue slots are 58 % used, the ALU pipe 50 %, DRAM 48 %.
+//
+// Shape.  Eight warps of a CTA take keys; one loads; three make the rotations' factors.  A
+// tile is `tile` keys of all KV heads of a head block: U sixteens of keys of one head for
+// each key warp.  It arrives by TMA as boxes of sixteen keys, in a ring of stages.  Two warps
+// a scheduler with U = 4 independent chains each beat four of U = 1 with half the registers
+// (51 against 61 us at 128K): what a warp does once a tile costs as much as a third of its
+// sixteen keys.  For head blocks below eight, U = 2 keeps two stages in shared memory.
 //
 // Matrix instructions: mma.m16n8k16 with the keys on M for the scores and the channels on M
-// for the values.  A lane expands the codes of its own fragment in registers: four to six
-// instructions make a register of two operands that the matrix instruction reads at once.
-// tcgen05 would need the expanded tile in shared memory: 2 bytes a code written and 2 read
-// beside the code's own half, 37 us of shared-memory time for 128K keys of eight heads,
-// where the codes take 23 us to arrive; expanded in registers they cost none.
+// for the values.  A lane expands the codes of its own fragments in registers.  tcgen05 would
+// need the expanded tile in shared memory: 2 bytes a code written and 2 read beside the code's
+// own half, 37 us of shared-memory time for 128K keys of eight heads, where the codes take 23
+// us to arrive; expanded in registers they cost none.
 //
 // Scores.  The codes less 8 are small integers, exact in fp16.  The query of each head is
 // scaled by a power of two to a largest channel in [8, 16) and split into two fp16 numbers,
@@ -143,22 +158,20 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 // moved, and products down to 2^-34 of the largest still count.  Numerator and denominator
 // share M, so it drops out.  Sums and outputs are held in fp32.
 //
-// The rotations' cos and sin are the same for all heads, so four warps make them once a tile
+// The rotations' cos and sin are the same for all heads, so three warps make them once a tile
 // for the whole head block: from the table's row of the tile's first key by steps of one
 // position in fp32, stored as fp16 in the order of the fragments.
 
 constexpr int kDecodeQ4Ctas = 148;  // one per SM
-constexpr int kDecodeQ4TabWarps = 3, kDecodeQ4OtherWarps = 1 + kDecodeQ4TabWarps;  // one loads
+constexpr int kDecodeQ4KeyWarps = 8, kDecodeQ4TurnWarps = 3, kDecodeQ4OtherWarps = 1 + kDecodeQ4TurnWarps;  // one loads
+constexpr int kDecodeQ4Threads = 32 * (kDecodeQ4KeyWarps + kDecodeQ4OtherWarps);
 constexpr int kDecodeQ4MaxStages = 6;
 
-// Key warps of a CTA, and the registers a thread at launch, of the key warps and of the others.
-template <int KW>
-struct DecodeQ4Warps {
-  static constexpr int kThreads = 32 * (KW + kDecodeQ4OtherWarps);
-  static constexpr int kRegs = KW == 8 ? 168 : 96, kKeyRegs = KW == 8 ? 216 : 104, kTabRegs = KW == 8 ? 72 : 64;
-  static_assert(KW * kKeyRegs + kDecodeQ4OtherWarps * kTabRegs <= (KW + kDecodeQ4OtherWarps) * kRegs,
-                "the split has to fit the launch's registers, or setmaxnreg waits for good");
-};
+// Registers a thread: 168 at launch; the key warps rise to 216, the others drop to 72.
+constexpr int kDecodeQ4Regs = 168, kDecodeQ4KeyRegs = 216, kDecodeQ4OtherRegs = 72;
+static_assert(kDecodeQ4KeyWarps * kDecodeQ4KeyRegs + kDecodeQ4OtherWarps * kDecodeQ4OtherRegs <=
+                  (kDecodeQ4KeyWarps + kDecodeQ4OtherWarps) * kDecodeQ4Regs,
+              "the split has to fit the launch's registers, or setmaxnreg waits for good");
 
 // Shared memory: a region for the query fragments, reused to join the key warps, then the
 // stages.  A stage: key codes, value codes, scales, cos/sin rows.
@@ -166,10 +179,10 @@ struct DecodeQ4Layout {
   int region, codes, scales, table, stage, stages, total;
 };
 
-// NQ: score tiles of four query heads; KW: key warps; HPB: KV heads of a block.
-__host__ __device__ constexpr DecodeQ4Layout decode_q4_layout(int D, int NQ, int KW, int HPB, int tile) {
+// NQ: score tiles of four query heads; HPB: KV heads of a block.
+__host__ __device__ constexpr DecodeQ4Layout decode_q4_layout(int D, int NQ, int HPB, int tile) {
   DecodeQ4Layout l{};
-  const int frags = 2 * HPB * NQ * (D / 32) * 512, join = KW * NQ * 4 * (D + 8) * 4;
+  const int frags = 2 * HPB * NQ * (D / 32) * 512, join = kDecodeQ4KeyWarps * NQ * 4 * (D + 8) * 4;
   l.region = ((frags > join ? frags : join) + 1023) / 1024 * 1024;
   l.codes = tile * HPB * D / 2;
   l.scales = tile * HPB * 16;
@@ -185,7 +198,7 @@ struct DecodeQ4Shared {
   uint64_t full[kDecodeQ4MaxStages];   // codes and scales have arrived, cos/sin rows are written
   uint64_t empty[kDecodeQ4MaxStages];
   float mul[32];                       // log2 units per unit of score, by query head of the block
-  float red_m[16][16], red_l[16][16];
+  float red_m[kDecodeQ4KeyWarps][16], red_l[kDecodeQ4KeyWarps][16];
   Q4Start start;
   int abort;
 };
@@ -206,9 +219,8 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-template <int KW>
 __device__ __forceinline__ void key_warps_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * KW) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kDecodeQ4KeyWarps) : "memory");
 }
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
@@ -239,11 +251,9 @@ constexpr uint32_t kEightsLow = 0x00080008u, kEightsHigh = 0x00800080u;
 __device__ __forceinline__ void prefetch_l2(const void* x) { asm volatile("prefetch.global.L2 [%0];" ::"l"(x)); }
 
 // Shared-memory loads by 32-bit address, in order with the barrier waits around them.
-template <int OFF = 0>
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4+%5];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at), "n"(OFF));
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
   return v;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t at) {
@@ -265,9 +275,8 @@ __device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(
 __device__ __forceinline__ int q4_key_of(int r) { return r ^ ((r & 1) << 2); }
 
 // A box holds sixteen keys in rows of neighbouring heads, 128 bytes where the block has that
-// many (TMA takes a row at a time: rows of 64 bytes, one head each, took twice as long as the
-// arithmetic), with the swizzle of that row length.  Bytes of a row of codes, and the offset
-// of byte x of key `key`'s row of `width` bytes.
+// many, with the swizzle of that row length.  Bytes of a row of codes, and the offset of byte x
+// of key `key`'s row of `width` bytes.
 __host__ __device__ constexpr int q4_code_row(int D, int HPB) { return HPB * D / 2 < 128 ? HPB * D / 2 : 128; }
 __device__ __forceinline__ int q4_at(int width, int key, int x) {
   const int turn = width == 128 ? key & 7 : width == 64 ? (key >> 1) & 3 : width == 32 ? (key >> 2) & 1 : 0;
@@ -280,8 +289,9 @@ __device__ __forceinline__ int q4_turn_at(int key, int w, int t) {
   return key * 2 * D + ((w * 64 + t * 16) ^ ((key & 1) << 6));  // neighbouring rows on different banks
 }
 
-template <int D, int NQ, int KEYS, int U>
-__global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
+// NQ: score tiles (of four query heads); U: sixteens of keys that a key warp takes at once.
+template <int D, int NQ, int U>
+__global__ void __launch_bounds__(kDecodeQ4Threads, 1)
     jl_decode_q4_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                         const __grid_constant__ CUtensorMap ts, const DecodeQ4Params p) {
   constexpr int HALF = D / 2;
@@ -295,7 +305,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
   __shared__ DecodeQ4Shared sh;
   uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   const int HPB = p.heads_per_block, T = p.tile;
-  const DecodeQ4Layout lay = decode_q4_layout(D, NQ, KEYS, HPB, T);
+  const DecodeQ4Layout lay = decode_q4_layout(D, NQ, HPB, T);
   uint8_t* const stages = smem + lay.region;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &sh.abort;
@@ -303,7 +313,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < lay.stages; ++s) {
       mbar_init(&sh.full[s], kDecodeQ4OtherWarps);
-      mbar_init(&sh.empty[s], KEYS);
+      mbar_init(&sh.empty[s], kDecodeQ4KeyWarps);
     }
     sh.abort = 0;
     fence_mbar_init();
@@ -331,10 +341,10 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
   int stage = 0;
   uint32_t phase = 0;
 
-  if (warp >= KEYS) {
-    setmaxnreg_dec<DecodeQ4Warps<KEYS>::kTabRegs>();
+  if (warp >= kDecodeQ4KeyWarps) {
+    setmaxnreg_dec<kDecodeQ4OtherRegs>();
     bool ok = true;
-    if (warp == KEYS) {
+    if (warp == kDecodeQ4KeyWarps) {
       // ---------------------------------------------------------------- loads --
       const int boxes = T / 16, rows = HPB * HALF / q4_code_row(D, HPB);  // of a tile; of codes, a key
       int issued = 0;
@@ -395,7 +405,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
     // (at most 88 steps: an error of some 2^-17 before the rounding to fp16).  Eight keys at a
     // time, each from a row of its own asked for eight keys ahead, took 27 us for 128K keys, the
     // rows' latency; one warp for all of a tile's rows took 43.
-    const int tw = warp - KEYS - 1;
+    const int tw = warp - kDecodeQ4KeyWarps - 1;
     // lane -> the two pairs of one packed register: word w, fragment lane t, register half e
     const bool has = D == 128 || lane < 16;
     const int w = D == 128 ? lane / 8 : (lane & 15) / 8, t = D == 128 ? (lane / 2) & 3 : lane & 3;
@@ -406,11 +416,11 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
     const uint64_t step_c = f2_pack(p.cos_tab[one + c0], p.cos_tab[one + c1]);
     const uint64_t step_s = f2_pack(p.sin_tab[one + c0], p.sin_tab[one + c1]);
     const uint64_t step_n = f2_pack(-p.sin_tab[one + c0], -p.sin_tab[one + c1]);
-    const int row0 = T / 8 * tw / kDecodeQ4TabWarps * 8, row1 = T / 8 * (tw + 1) / kDecodeQ4TabWarps * 8;
+    const int row0 = T / 8 * tw / kDecodeQ4TurnWarps * 8, row1 = T / 8 * (tw + 1) / kDecodeQ4TurnWarps * 8;
     while (cur < st.end && ok) {
       const int tiles = q4_tiles(p, L);
       const int t1 = min(tiles, t0 + (st.end - cur));
-      const int grow = max(1, (L + p.w_pre - 1) / p.w_pre);
+      const int grow = q4_group(p, L);
       const int jb = grow > 1 ? L - 1 - p.w0 : -1;  // remote keys are j <= jb
       const int far_tiles = jb < 0 ? 0 : min(t1, jb / T + 1);
       float2 next_c = make_float2(1.f, 1.f), next_s = make_float2(0.f, 0.f);
@@ -419,6 +429,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
         const int quot = j / grow;
         next_left = grow - (j - quot * grow);  // keys until f steps; that key keeps the angle of the one before it
         const int64_t row = min(static_cast<int64_t>(j - quot), p.n_tab_rows - 1) * HALF;  // behind the length: none
+        JL_CHECK(j >= 0 && quot >= 0 && quot <= j && (j >= L || j - quot < p.n_tab_rows));
         next_c = make_float2(p.cos_tab[row + c0], p.cos_tab[row + c1]);
         next_s = make_float2(p.sin_tab[row + c0], p.sin_tab[row + c1]);
       };
@@ -478,9 +489,9 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
   }
 
   // ------------------------------------------------------------------ the keys --
-  setmaxnreg_inc<DecodeQ4Warps<KEYS>::kKeyRegs>();
+  setmaxnreg_inc<kDecodeQ4KeyRegs>();
   const int g = lane >> 2, t = lane & 3;
-  const int wph = KEYS / HPB;                          // warps that share a head
+  const int wph = kDecodeQ4KeyWarps / HPB;                          // warps that share a head
   const int wsub = warp % wph, head = warp / wph;      // this warp's place among them, its KV head in the block
   const int keyA = q4_key_of(g);                       // its score rows' keys of a sixteen: keyA, keyA + 8
   const int key0 = q4_key_of(2 * t), key1 = q4_key_of(2 * t + 1);  // its value fragments': these and 8 on
@@ -504,13 +515,13 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
     const int tiles = q4_tiles(p, L);
     const int t1 = min(tiles, t0 + (st.end - cur));
     if (t1 > t0) {
-      const int i = L - 1, grow = max(1, (L + p.w_pre - 1) / p.w_pre);
+      const int i = L - 1, grow = q4_group(p, L);
       const int jb = grow > 1 ? i - p.w0 : -1;
 
       // Query fragments: this warp's query heads of the block, local and remote variant, each
       // split into two fp16 columns.  All loads come first.
       {
-        constexpr int kRows = 32 / KEYS;  // HPB * NQ <= 8
+        constexpr int kRows = 32 / kDecodeQ4KeyWarps;  // HPB * NQ <= 8
         const int nq = i - i / grow;
         const bool has = D == 128 || lane < 16;
         const int w = D == 128 ? lane / 8 : (lane & 15) / 8, ft = D == 128 ? (lane / 2) & 3 : lane & 3;
@@ -519,7 +530,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
         float y[kRows][4];  // channels c0, c1, c0 + D/2, c1 + D/2
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-          const int x = warp + u * KEYS, h = x / (4 * NQ), qh = x % (4 * NQ);  // KV head, query head of its group
+          const int x = warp + u * kDecodeQ4KeyWarps, h = x / (4 * NQ), qh = x % (4 * NQ);  // KV head, query head of its group
 #pragma unroll
           for (int n = 0; n < 4; ++n) y[u][n] = 0.f;
           if (h < HPB && qh < p.group && has) {
@@ -541,7 +552,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
           for (int u = 0; u < kRows; ++u) top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-          const int x = warp + u * KEYS, h = x / (4 * NQ), qh = x % (4 * NQ);
+          const int x = warp + u * kDecodeQ4KeyWarps, h = x / (4 * NQ), qh = x % (4 * NQ);
           // 2^up brings the largest channel into [8, 16); up in [-120, 120] keeps both factors normal
           const int up = min(120, max(-120, 130 - static_cast<int>(__float_as_uint(top[u]) >> 23)));
           const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
@@ -569,7 +580,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
           }
         }
       }
-      key_warps_sync<KEYS>();
+      key_warps_sync();
 
       float o[NP][MT][4], eights[NP][kF][4], m[NQ], l[NQ], mul[NQ];
       uint4 qf[kQueryRegs ? NQ * KW : 1];
@@ -594,6 +605,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
       for (int tile = t0; tile < t1; ++tile, j += T) {
         if (ok) ok = warp_wait(&sh.full[stage], phase, abort);
         if (ok && j < L) {
+          JL_CHECK(tile < tiles && j >= 0 && L <= p.max_seqlen && head < HPB && hb * HPB + head < p.Hkv);
           const uint32_t base = stages_at + stage * lay.stage;
           const uint32_t ka = base + at_key, sa = base + at_scale;
           uint32_t kc[U][2][KW];
@@ -864,7 +876,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
           }
         }
       } else {
-      key_warps_sync<KEYS>();  // every warp is done with the query fragments
+      key_warps_sync();  // every warp is done with the query fragments
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         if (g == 0) {
@@ -880,8 +892,8 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
           row[16 * x + 8] = (o[n / 2][x][2 + y] - eights[n / 2][f][2 + y]) * 0x1p20f;
         }
       }
-      key_warps_sync<KEYS>();
-      for (int x = threadIdx.x; x < hpb * (D / 4); x += 32 * KEYS) {
+      key_warps_sync();
+      for (int x = threadIdx.x; x < hpb * (D / 4); x += 32 * kDecodeQ4KeyWarps) {
         const int q = x / (D / 4), c = x % (D / 4) * 4;  // query head of the block, its channels c .. c + 3
         const int in = q % p.group, w0 = q / p.group * wph;
         float mx = -INFINITY;
@@ -913,7 +925,7 @@ __global__ void __launch_bounds__(DecodeQ4Warps<KEYS>::kThreads, 1)
         }
       }
       }
-      key_warps_sync<KEYS>();  // the region is free for the next segment's query
+      key_warps_sync();  // the region is free for the next segment's query
     }
     cur += t1 - t0;
     t0 = 0;
