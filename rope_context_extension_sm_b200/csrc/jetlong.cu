@@ -749,15 +749,17 @@ jl_status launch_decode_q4(const jl::DecodeQ4Params& prm, cudaStream_t st) {
 template <int D>
 jl_status dispatch_decode_q4(jl::DecodeQ4Params& prm, cudaStream_t st) {
   // Score tiles of four query heads (two columns each in an n = 8 matrix instruction); KV heads
-  // of a block, which share its cos/sin rows, as many as eight key warps and
-  // 32 KB of query fragments allow; sixteens of keys that a warp takes at once: four chains
-  // hide more latency than two (47.8 against 50.5 us at 128K keys, 32/8 heads), but smaller head
-  // blocks have longer tiles and would be left with one stage in shared memory, and more score
-  // tiles have chains enough and no registers.
+  // of a block, which share its cos/sin rows, as many as eight key warps and 32 KB of query
+  // fragments allow; sixteens of keys that a warp takes at once.  Four chains hide more latency
+  // than two, and two more than one: at 128K keys of 128 channels 47.8 us against 50.5 for 32/8
+  // heads, and, two against one, 36.8 against 40.6 for 32/4.  A head block below eight has longer
+  // tiles, and four would leave it one stage of shared memory; so would two with eight query
+  // heads a KV head and a block of one (24/3 heads: 46.7 us against 39.1 with one).  Sixteen
+  // query heads leave no registers for two.
   const int nq = prm.group <= 4 ? 1 : prm.group <= 8 ? 2 : 4;
   int hpb = 8 / nq;
   while (prm.Hkv % hpb != 0) hpb /= 2;
-  const int sixteens = nq > 1 ? 1 : hpb == 8 ? 4 : 2;
+  const int sixteens = hpb == 8 ? 4 : nq == 1 || (nq == 2 && hpb > 1) ? 2 : 1;
   prm.heads_per_block = hpb;
   prm.tile = 16 * sixteens * 8 / hpb;
   prm.tile_log2 = __builtin_ctz(prm.tile);
@@ -765,7 +767,7 @@ jl_status dispatch_decode_q4(jl::DecodeQ4Params& prm, cudaStream_t st) {
   if (tiles > 0x7fffffff) return fail(JL_ERR_UNSUPPORTED, "too many keys for one call (%lld tiles)", (long long)tiles);
   prm.n_cta = static_cast<int32_t>(std::min<int64_t>(jl::kDecodeQ4Ctas, tiles));
   if (nq == 4) return launch_decode_q4<D, 4, 1>(prm, st);
-  if (nq == 2) return launch_decode_q4<D, 2, 1>(prm, st);
+  if (nq == 2) return sixteens == 2 ? launch_decode_q4<D, 2, 2>(prm, st) : launch_decode_q4<D, 2, 1>(prm, st);
   return sixteens == 4 ? launch_decode_q4<D, 1, 4>(prm, st) : launch_decode_q4<D, 1, 2>(prm, st);
 }
 
