@@ -422,7 +422,7 @@ jl_status jl_decode_append_paged(const void* q, const void* k, const void* v, co
  *   k_out[b][p - starts[b]] and v_out[b][p - starts[b]], bf16 [B][out_rows][Hkv][head_dim]
  * (one rounding of the exact product), base-RoPE keys as jl_bifocal_prefill_chunk and
  * jl_bifocal_decode take them.  starts: device int32 [B], NULL means 0; lens: device int32
- * [B].  Needs 0 <= starts[b], lens[b] <= cache_stride and lens[b] - starts[b] <= out_rows;
+ * [B <= 65535].  Needs 0 <= starts[b], lens[b] <= cache_stride and lens[b] - starts[b] <= out_rows;
  * an entry outside that, and a page index outside the pool, are skipped and reported by
  * jl_sync_status() as JL_ERR_INVALID.  Output rows behind lens[b] - starts[b] are left as
  * they were.
@@ -471,7 +471,9 @@ jl_status jl_kv_cache_read_q4_paged(const void* k_codes, const void* v_codes, co
  * Cache rows behind an entry's length may hold anything, NaN scales too.  Paged: page_size
  * is a multiple of 16; a page outside [0, num_pages) is read as zeros and reported by
  * jl_sync_status() as JL_ERR_INVALID.  Supported: head_dim 64 or 128, 1 to 16 query heads
- * per KV head, B <= 65535.
+ * per KV head, B and Hkv up to 65535.  The result does not depend on the order in which the
+ * CTAs run (no atomics), but on how the batch's keys are shared out: the same entry in another
+ * batch may differ in the last bits.
  */
 jl_status jl_bifocal_decode_q4(const void* q, const void* k_codes, const void* v_codes, const void* scales,
                                const int32_t* seqlens, int32_t B, int64_t cache_stride, int32_t max_seqlen,

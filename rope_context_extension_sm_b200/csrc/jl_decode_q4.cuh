@@ -329,9 +329,9 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
     if (__any_sync(0xffffffffu, failed)) s.end = s.begin;
     if (lane == 0) sh.start = s;
   } else if (warp == 1) {
-    // The queries of a small batch are asked for before the loads of the tiles, behind which
-    // they would queue for some microseconds.
-    const int bytes = p.B <= 16 ? min(p.B * p.Hq * D * 2, 16384) : 0;
+    // The first queries are asked for before the loads of the tiles, behind which they would
+    // queue for some microseconds; a small batch has no others.
+    const int64_t bytes = min(static_cast<int64_t>(p.B) * p.Hq * D * 2, static_cast<int64_t>(16384));
     for (int x = lane * 128; x < bytes; x += 32 * 128) prefetch_l2(reinterpret_cast<const char*>(p.q) + x);
   }
   __syncthreads();

@@ -490,10 +490,10 @@ def _q4_cache(k_codes, v_codes, scales, block_table, batch: int):
     head_dim, the three addresses, and where an entry's rows are: (stride,) or (table, max_pages,
     page_size, num_pages)."""
     shape, dev = k_codes.shape, k_codes.get_device()
-    if len(shape) != 4 or dev < 0:
+    if len(shape) != 4 or dev < 0 or k_codes.dtype is not _U8 or not k_codes.is_contiguous():
         _need(k_codes, _U8, "k_codes", 4)
     n, rows, hkv, half = shape
-    at = (_q4_is(k_codes, _U8, shape, dev, "k_codes"), _q4_is(v_codes, _U8, shape, dev, "v_codes"),
+    at = (k_codes.data_ptr(), _q4_is(v_codes, _U8, shape, dev, "v_codes"),
           _q4_is(scales, _BF16, (n, rows, hkv, 8), dev, "scales"))
     if block_table is None:
         if n != batch:
@@ -563,15 +563,19 @@ def _append_q4(name, q, k, v, seqlens, cos, sin, k_codes, v_codes, scales, q_out
         _need(q, _BF16, "q", 3)
     B, hq = shape[:2]
     dev, hkv, d, cache, where = _q4_cache(k_codes, v_codes, scales, block_table, B)
-    if q_out is None:
+    q_at = _q4_is(q, _BF16, (B, hq, d), dev, "q")
+    if q_out is not None:
+        q_out_at = _q4_is(q_out, _BF16, shape, dev, "q_out")
+    else:
         if stream is None:
             q_out = torch.empty_like(q)
         else:
             with _q4_alloc(stream, dev):
                 q_out = torch.empty_like(q)
-    _q4_call(name, stream, dev, _q4_is(q, _BF16, (B, hq, d), dev, "q"), _q4_is(k, _BF16, (B, hkv, d), dev, "k"),
+        q_out_at = q_out.data_ptr()
+    _q4_call(name, stream, dev, q_at, _q4_is(k, _BF16, (B, hkv, d), dev, "k"),
              _q4_is(v, _BF16, (B, hkv, d), dev, "v"), _q4_is(seqlens, _I32, (B,), dev, "seqlens"), B, hq, hkv, d,
-             *_q4_tables(cos, sin, d, dev), _q4_is(q_out, _BF16, shape, dev, "q_out"), *cache, *where)
+             *_q4_tables(cos, sin, d, dev), q_out_at, *cache, *where)
     return q_out
 
 
@@ -630,36 +634,44 @@ def _decode_q4_workspace(hq: int, d: int) -> int:
     return int(_lib.jl_bifocal_decode_q4_workspace_size(hq, d))
 
 
-def _decode_q4_outputs(q, B, hq, d, out, lse, workspace, want_lse):
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None and want_lse:
-        lse = q.new_empty((B, hq), dtype=_F32)
-    if workspace is None:
-        workspace = q.new_empty(_decode_q4_workspace(hq, d), dtype=_U8)
-    return out, lse, workspace
-
-
 def _decode_q4(name, q, k_codes, v_codes, scales, seqlens, max_seqlen, w0, w_pretrained, cos, sin, softmax_scale, out,
                lse, workspace, want_lse, stream, block_table):
     shape = q.shape
     if len(shape) != 3:
         _need(q, _BF16, "q", 3)
-    B, hq = shape[:2]
+    B, hq, _ = shape
     dev, hkv, d, cache, where = _q4_cache(k_codes, v_codes, scales, block_table, B)
-    if stream is None:
-        out, lse, workspace = _decode_q4_outputs(q, B, hq, d, out, lse, workspace, want_lse)
+    q_at = _q4_is(q, _BF16, (B, hq, d), dev, "q")
+    # the caller's outputs are checked, new ones need no check
+    out_at = None if out is None else _q4_is(out, _BF16, shape, dev, "out")
+    lse_at = None if lse is None else _q4_is(lse, _F32, (B, hq), dev, "lse")
+    if workspace is None:
+        ws_bytes = _decode_q4_workspace(hq, d)
+    elif workspace.get_device() == dev and workspace.is_contiguous():
+        ws_bytes = workspace.numel() * workspace.element_size()
     else:
-        with _q4_alloc(stream, dev):
-            out, lse, workspace = _decode_q4_outputs(q, B, hq, d, out, lse, workspace, want_lse)
-    if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the cache's device")
+    if stream is None:
+        context = None
+    else:
+        context = _q4_alloc(stream, dev)
+        context.__enter__()
+    try:
+        if out is None:
+            out = torch.empty_like(q)
+            out_at = out.data_ptr()
+        if lse is None and want_lse:
+            lse = q.new_empty((B, hq), dtype=_F32)
+            lse_at = lse.data_ptr()
+        if workspace is None:
+            workspace = q.new_empty(ws_bytes, dtype=_U8)
+    finally:
+        if context is not None:
+            context.__exit__(None, None, None)
     lens = _q4_is(seqlens, _I32, (B,), dev, "seqlens")
     where = (lens, B, *where) if block_table is None else (where[0], lens, B, *where[1:])
-    _q4_call(name, stream, dev, _q4_is(q, _BF16, (B, hq, d), dev, "q"), *cache, *where, max_seqlen, hq, hkv, d, w0,
-             w_pretrained, *_q4_tables(cos, sin, d, dev), softmax_scale, _q4_is(out, _BF16, shape, dev, "out"),
-             None if lse is None else _q4_is(lse, _F32, (B, hq), dev, "lse"), workspace.data_ptr(),
-             workspace.numel() * workspace.element_size())
+    _q4_call(name, stream, dev, q_at, *cache, *where, max_seqlen, hq, hkv, d, w0, w_pretrained,
+             *_q4_tables(cos, sin, d, dev), softmax_scale, out_at, lse_at, workspace.data_ptr(), ws_bytes)
     return out, lse
 
 
