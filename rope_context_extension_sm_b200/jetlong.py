@@ -467,6 +467,7 @@ def jl_kv_cache_q4_empty(n: int, stride: int, n_kv_heads: int, head_dim: int, *,
 # The checks below run for every token that a serving loop decodes, so each tensor is checked in one
 # expression, and only a failed one is looked at again for its message.
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_same_stream = contextlib.nullcontext()
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
@@ -567,11 +568,8 @@ def _append_q4(name, q, k, v, seqlens, cos, sin, k_codes, v_codes, scales, q_out
     if q_out is not None:
         q_out_at = _q4_is(q_out, _BF16, shape, dev, "q_out")
     else:
-        if stream is None:
+        with _same_stream if stream is None else _q4_alloc(stream, dev):
             q_out = torch.empty_like(q)
-        else:
-            with _q4_alloc(stream, dev):
-                q_out = torch.empty_like(q)
         q_out_at = q_out.data_ptr()
     _q4_call(name, stream, dev, q_at, _q4_is(k, _BF16, (B, hkv, d), dev, "k"),
              _q4_is(v, _BF16, (B, hkv, d), dev, "v"), _q4_is(seqlens, _I32, (B,), dev, "seqlens"), B, hq, hkv, d,
@@ -600,7 +598,7 @@ def _read_q4(name, k_codes, v_codes, scales, lens, starts, k_out, v_out, rows, s
         rows = given.shape[1] if given is not None else where[0] if block_table is None else where[1] * where[2]
     shape = (B, rows, hkv, d)
     if k_out is None or v_out is None:
-        with contextlib.nullcontext() if stream is None else _q4_alloc(stream, dev):
+        with _same_stream if stream is None else _q4_alloc(stream, dev):
             k_out = scales.new_empty(shape) if k_out is None else k_out
             v_out = scales.new_empty(shape) if v_out is None else v_out
     _q4_call(name, stream, dev, *cache, *where,
@@ -642,6 +640,7 @@ def _decode_q4(name, q, k_codes, v_codes, scales, seqlens, max_seqlen, w0, w_pre
     B, hq, _ = shape
     dev, hkv, d, cache, where = _q4_cache(k_codes, v_codes, scales, block_table, B)
     q_at = _q4_is(q, _BF16, (B, hq, d), dev, "q")
+    tables = _q4_tables(cos, sin, d, dev)
     # the caller's outputs are checked, new ones need no check
     out_at = None if out is None else _q4_is(out, _BF16, shape, dev, "out")
     lse_at = None if lse is None else _q4_is(lse, _F32, (B, hq), dev, "lse")
@@ -651,27 +650,19 @@ def _decode_q4(name, q, k_codes, v_codes, scales, seqlens, max_seqlen, w0, w_pre
         ws_bytes = workspace.numel() * workspace.element_size()
     else:
         raise ValueError("workspace must be a contiguous CUDA tensor on the cache's device")
-    if stream is None:
-        context = None
-    else:
-        context = _q4_alloc(stream, dev)
-        context.__enter__()
-    try:
+    with _same_stream if stream is None else _q4_alloc(stream, dev):
         if out is None:
             out = torch.empty_like(q)
             out_at = out.data_ptr()
         if lse is None and want_lse:
-            lse = q.new_empty((B, hq), dtype=_F32)
+            lse = cos.new_empty((B, hq))  # fp32, as the tables were checked to be
             lse_at = lse.data_ptr()
         if workspace is None:
-            workspace = q.new_empty(ws_bytes, dtype=_U8)
-    finally:
-        if context is not None:
-            context.__exit__(None, None, None)
+            workspace = k_codes.new_empty(ws_bytes)  # bytes
     lens = _q4_is(seqlens, _I32, (B,), dev, "seqlens")
     where = (lens, B, *where) if block_table is None else (where[0], lens, B, *where[1:])
     _q4_call(name, stream, dev, q_at, *cache, *where, max_seqlen, hq, hkv, d, w0, w_pretrained,
-             *_q4_tables(cos, sin, d, dev), softmax_scale, out_at, lse_at, workspace.data_ptr(), ws_bytes)
+             *tables, softmax_scale, out_at, lse_at, workspace.data_ptr(), ws_bytes)
     return out, lse
 
 
