@@ -750,9 +750,9 @@ template <int D>
 jl_status dispatch_decode_q4(jl::DecodeQ4Params& prm, cudaStream_t st) {
   // Score tiles of four query heads (two columns each in an n = 8 matrix instruction); KV heads
   // of a block, which share its cos/sin rows, as many as eight key warps and 32 KB of query
-  // fragments allow; sixteens of keys that a warp takes at once.  Four chains hide more latency
-  // than two, and two more than one: at 128K keys of 128 channels 47.8 us against 50.5 for 32/8
-  // heads, and, two against one, 36.8 against 40.6 for 32/4.  A head block below eight has longer
+  // fragments allow; sixteens of keys of a warp in a tile.  Four hide more latency
+  // than two, and two more than one: at 128K keys of 128 channels 45.9 us against 50.5 for 32/8
+  // heads, and, two against one, 36.1 against 40.6 for 32/4.  A head block below eight has longer
   // tiles, and four would leave it one stage of shared memory; so would two with eight query
   // heads a KV head and a block of one (24/3 heads: 46.7 us against 39.1 with one).  Sixteen
   // query heads leave no registers for two.

@@ -91,7 +91,7 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
   const int total = all * (p.Hkv / p.heads_per_block);
   const int per = q4_per_cta(p, total);
   s.begin = min(static_cast<int64_t>(total), static_cast<int64_t>(per) * blockIdx.x);
-  s.end = min(total, s.begin + per);
+  s.end = s.begin + min(per, total - s.begin);
   if (s.begin >= s.end) return s;
   s.hb = s.begin / all;
   int left = s.begin % all;
@@ -132,9 +132,10 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 // Shape.  Eight warps of a CTA take keys; one loads; three make the rotations' factors.  A
 // tile is `tile` keys of all KV heads of a head block: U sixteens of keys of one head for
 // each key warp.  It arrives by TMA as boxes of sixteen keys, in a ring of stages.  Two warps
-// a scheduler with U = 4 independent chains each beat four of U = 1 with half the registers
-// (51 against 61 us at 128K): what a warp does once a tile costs as much as a third of its
-// sixteen keys.  For head blocks below eight, U = 2 keeps two stages in shared memory.
+// a scheduler with U = 4 beat four of U = 1 with half the registers (51 against 61 us at
+// 128K): what a warp does once a tile costs as much as a third of its sixteen keys.  The values
+// of one sixteen stand beside the scores of the next, independent of them and on other pipes:
+// 45.9 us, against 47.8 with the scores of all four side by side, which keeps them apart.  For head blocks below eight, U = 2 keeps two stages in shared memory.
 //
 // Matrix instructions: mma.m16n8k16 with the keys on M for the scores and the channels on M
 // for the values.  A lane expands the codes of its own fragments in registers.  tcgen05 would
@@ -289,7 +290,7 @@ __device__ __forceinline__ int q4_turn_at(int key, int w, int t) {
   return key * 2 * D + ((w * 64 + t * 16) ^ ((key & 1) << 6));  // neighbouring rows on different banks
 }
 
-// NQ: score tiles (of four query heads); U: sixteens of keys that a key warp takes at once.
+// NQ: score tiles (of four query heads); U: sixteens of keys of a key warp in a tile.
 template <int D, int NQ, int U>
 __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
     jl_decode_q4_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -601,235 +602,236 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
           for (int f = 0; f < kF; ++f) eights[n][f][y] = 0.f;
         }
 
-      int j = t0 * T + wsub * 16 * U;  // the warp's first key of the tile
-      for (int tile = t0; tile < t1; ++tile, j += T) {
-        if (ok) ok = warp_wait(&sh.full[stage], phase, abort);
-        if (ok && j < L) {
-          JL_CHECK(tile < tiles && j >= 0 && L <= p.max_seqlen && head < HPB && hb * HPB + head < p.Hkv);
-          const uint32_t base = stages_at + stage * lay.stage;
-          const uint32_t ka = base + at_key, sa = base + at_scale;
-          uint32_t kc[U][2][KW];
-          uint2 ks[U][2];
+      uint32_t base = 0;         // the stage's address
+      int j = 0;                 // first key of the sixteen at hand
+      uint32_t pf[NP][kF][2];    // weight fragments of the sixteen before it
+
+      // Scores of sixteen keys under one variant of the query (and, far, of the keys); rows g and
+      // g + 8, head 4 n + t.
+      auto scores = [&](auto far_tag, int u, float (&dst)[NQ][2]) {
+        constexpr bool FAR = decltype(far_tag)::value;
+        const uint32_t fa = frags_at + (FAR ? far_frags : 0u);
+        if constexpr (kQueryRegs) {
+          if (have != FAR) {
+            have = FAR;
 #pragma unroll
-          for (int u = 0; u < U; ++u)
+            for (int x = 0; x < NQ * KW; ++x) qf[x] = lds128(fa + x * 512);
+          }
+        }
+        uint32_t kc[2][KW];
+        uint2 ks[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t at = base + at_key + u * next_codes + r * eight;
+          if constexpr (D == 128) {
+            const uint4 v = lds128(at);
+            kc[r][0] = v.x, kc[r][1] = v.y, kc[r][2] = v.z, kc[r][3] = v.w;
+          } else {
+            const uint2 v = lds64(at);
+            kc[r][0] = v.x, kc[r][1] = v.y;
+          }
+          ks[r] = lds64(base + at_scale + u * next_scales + r * 128 * HPB);
+        }
+        const uint32_t turn0 = base + at_turn0 + u * 32 * D, turn1 = base + at_turn1 + u * 32 * D;
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) dst[n][0] = dst[n][1] = 0.f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          uint4 turn[2];
+          if constexpr (FAR) {
+            turn[0] = lds128((w & 1 ? turn1 : turn0) + (w >> 1) * 128);
+            turn[1] = lds128((w & 1 ? turn1 : turn0) + (w >> 1) * 128 + 16 * D);
+          }
+          uint32_t lo[2][2], hi[2][2];  // [row][register half]
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t word = e ? kc[r][w] >> 8 : kc[r][w];
+              __half2 a = codes_f16<false>(word), bb = codes_f16<true>(word);
+              if constexpr (FAR) {  // R(-n)
+                const __half2 c = bits_h2(e ? turn[r].y : turn[r].x), sn = bits_h2(e ? turn[r].w : turn[r].z);
+                const __half2 na = __hfma2(a, c, __hmul2(bb, sn));
+                bb = __hfma2(bb, c, __hneg2(__hmul2(a, sn)));
+                a = na;
+              }
+              lo[r][e] = h2_bits(a);
+              hi[r][e] = h2_bits(bb);
+            }
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            uint4 q;
+            if constexpr (kQueryRegs) q = qf[n * KW + w];
+            else q = lds128(fa + (n * KW + w) * 512);
+            if constexpr (D == 128) {  // a word is one group: two steps, low channels then high
+              float c[4];
+              mma_f16_zero(c, {lo[0][0], lo[1][0], lo[0][1], lo[1][1]}, q.x, q.y);
+              mma_f16(c, {hi[0][0], hi[1][0], hi[0][1], hi[1][1]}, q.z, q.w);
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const uint32_t sc = w < 2 ? ks[r].x : ks[r].y;
+                dst[n][r] = fmaf(w & 1 ? bf16_high(sc) : bf16_low(sc), c[2 * r] + c[2 * r + 1], dst[n][r]);
+              }
+            } else {  // two groups, a step each
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float c[4];
+                mma_f16_zero(c, {lo[0][e], lo[1][e], hi[0][e], hi[1][e]}, e ? q.z : q.x, e ? q.w : q.y);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const uint32_t sc = w == 0 ? ks[r].x : ks[r].y;
+                  dst[n][r] = fmaf(e ? bf16_high(sc) : bf16_low(sc), c[2 * r] + c[2 * r + 1], dst[n][r]);
+                }
+              }
+            }
+          }
+        }
+      };
+
+      // Weights of sixteen keys and their products with the value scales.  M moves only when a
+      // product passes 2^14 (in the first keys: by anything), so it rarely does.
+      auto weights = [&](int u, float (&s)[NQ][2], auto tail_tag) {
+        constexpr bool TAIL = decltype(tail_tag)::value;
+        uint2 vs[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          vs[r] = lds64(base + at_scale + u * next_scales + r * 128 * HPB + 8);
+          if (TAIL && j + keyA + 8 * r >= L) {  // behind the length: weight 0, and no NaN scale that it could meet
+            vs[r] = make_uint2(0u, 0u);
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) s[n][r] = -INFINITY;
+          }
+        }
+        float wt[NQ][2], vf[2][4];
+        bool over = false;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          vf[r][0] = bf16_low(vs[r].x), vf[r][1] = bf16_high(vs[r].x), vf[r][2] = bf16_low(vs[r].y), vf[r][3] = bf16_high(vs[r].y);
+          const float top = fmaxf(fmax3(vf[r][0], vf[r][1], vf[r][2]), fmaxf(vf[r][3], 0x1p-90f));
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            wt[n][r] = ex2_approx(fmaf(s[n][r], mul[n], -m[n]));
+            over |= wt[n][r] * top > 0x1p14f;
+          }
+        }
+        if (__any_sync(0xffffffffu, over)) {
+          float f[NQ];
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            float top = m[n] + 10.f;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const uint32_t at = ka + u * next_codes + r * eight;
-              if constexpr (D == 128) {
-                const uint4 v = lds128(at);
-                kc[u][r][0] = v.x, kc[u][r][1] = v.y, kc[u][r][2] = v.z, kc[u][r][3] = v.w;
-              } else {
-                const uint2 v = lds64(at);
-                kc[u][r][0] = v.x, kc[u][r][1] = v.y;
-              }
-              ks[u][r] = lds64(sa + u * next_scales + r * 128 * HPB);
+              const float big = fmaxf(fmax3(vf[r][0], vf[r][1], vf[r][2]), fmaxf(vf[r][3], 0x1p-90f));
+              top = fmaxf(top, fmaf(s[n][r], mul[n], __log2f(big)));
             }
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const float now = top - 10.f;
+            f[n] = m[n] == -INFINITY ? 0.f : ex2_approx(m[n] - now);
+            m[n] = now;
+            l[n] *= f[n];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) wt[n][r] = ex2_approx(fmaf(s[n][r], mul[n], -now));
+          }
+#pragma unroll
+          for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float by = f[NQ == 1 ? 0 : 2 * n + (y & 1)];
+#pragma unroll
+              for (int x = 0; x < MT; ++x) o[n][x][y] *= by;
+#pragma unroll
+              for (int x = 0; x < kF; ++x) eights[n][x][y] *= by;
+            }
+        }
+        // Column 2t of the weights is head t of score tile 2n, column 2t + 1 of tile 2n + 1; with
+        // one score tile both are head t, the even columns under the scales of the even groups
+        // and the odd ones under those of the odd groups.
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) l[n] += wt[n][r];
+#pragma unroll
+          for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int f = 0; f < kF; ++f) {
+              const float a = wt[NQ == 1 ? 0 : 2 * n][r] * vf[r][NQ == 1 ? 2 * f : f];
+              const float bb = wt[NQ == 1 ? 0 : 2 * n + 1][r] * vf[r][NQ == 1 ? 2 * f + 1 : f];
+              pf[n][f][r] = transpose_8x8(h2_bits(__floats2half2_rn(a, bb)));
+            }
+        }
+      };
 
-          // Scores under one variant of the query (and, far, of the keys); rows g and g + 8 of
-          // each sixteen, head 4 n + t.
-          float s[U][NQ][2];
-          auto scores = [&](auto far_tag, auto& dst) {
-            constexpr bool FAR = decltype(far_tag)::value;
-            const uint32_t fa = frags_at + (FAR ? far_frags : 0u);
-            if constexpr (kQueryRegs) {
-              if (have != FAR) {
-                have = FAR;
+      auto values = [&](int u) {
+        uint32_t vc[4][VW];  // value codes of keys key0, key1, key0 + 8, key1 + 8
 #pragma unroll
-                for (int x = 0; x < NQ * KW; ++x) qf[x] = lds128(fa + x * 512);
-              }
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t at = base + (r & 1 ? at_val1 : at_val0) + u * next_codes + (r >> 1) * eight;
+          if constexpr (D == 128) {
+            const uint2 v = lds64(at);
+            vc[r][0] = v.x, vc[r][1] = v.y;
+          } else {
+            vc[r][0] = lds32(at);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+#pragma unroll
+          for (int f = 0; f < kF; ++f)
+            mma_f16(eights[n][f], {kEightsLow, kEightsHigh, kEightsLow, kEightsHigh}, pf[n][f][0], pf[n][f][1]);
+#pragma unroll
+        for (int w = 0; w < VW; ++w)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t pick = y ? 0x7632u : 0x5410u;
+            const uint32_t a = __byte_perm(vc[0][w], vc[1][w], pick), bb = __byte_perm(vc[2][w], vc[3][w], pick);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {  // channel tile x: byte 2y + z of word w
+              const int x = 4 * w + 2 * y + z, f = NQ == 1 ? x * 2 / MT : x * 4 / MT;
+              const uint32_t az = a >> (8 * z), bz = bb >> (8 * z);
+              const uint32_t frag[4] = {az & 0x000f000fu, az & 0x00f000f0u, bz & 0x000f000fu, bz & 0x00f000f0u};
+#pragma unroll
+              for (int n = 0; n < NP; ++n) mma_f16(o[n][x], frag, pf[n][f][0], pf[n][f][1]);
             }
-            const uint32_t turn0 = base + at_turn0, turn1 = base + at_turn1;
+          }
+      };
+
+      // A tile that is all local or all remote: the values of one sixteen beside the scores of the
+      // next, whose instructions keep different pipes busy.
+      auto whole_tile = [&](auto far_tag) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-              for (int n = 0; n < NQ; ++n) dst[u][n][0] = dst[u][n][1] = 0.f;
-#pragma unroll
-            for (int w = 0; w < KW; ++w)
-#pragma unroll
-              for (int u = 0; u < U; ++u) {
-                uint4 turn[2];
-                if constexpr (FAR) {
-                  turn[0] = lds128((w & 1 ? turn1 : turn0) + u * 32 * D + (w >> 1) * 128);
-                  turn[1] = lds128((w & 1 ? turn1 : turn0) + u * 32 * D + (w >> 1) * 128 + 16 * D);
-                }
-                uint32_t lo[2][2], hi[2][2];  // [row][register half]
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    const uint32_t word = e ? kc[u][r][w] >> 8 : kc[u][r][w];
-                    __half2 a = codes_f16<false>(word), bb = codes_f16<true>(word);
-                    if constexpr (FAR) {  // R(-n)
-                      const __half2 c = bits_h2(e ? turn[r].y : turn[r].x), sn = bits_h2(e ? turn[r].w : turn[r].z);
-                      const __half2 na = __hfma2(a, c, __hmul2(bb, sn));
-                      bb = __hfma2(bb, c, __hneg2(__hmul2(a, sn)));
-                      a = na;
-                    }
-                    lo[r][e] = h2_bits(a);
-                    hi[r][e] = h2_bits(bb);
-                  }
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                  uint4 q;
-                  if constexpr (kQueryRegs) q = qf[n * KW + w];
-                  else q = lds128(fa + (n * KW + w) * 512);
-                  if constexpr (D == 128) {  // a word is one group: two steps, low channels then high
-                    float c[4];
-                    mma_f16_zero(c, {lo[0][0], lo[1][0], lo[0][1], lo[1][1]}, q.x, q.y);
-                    mma_f16(c, {hi[0][0], hi[1][0], hi[0][1], hi[1][1]}, q.z, q.w);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                      const uint32_t sc = w < 2 ? ks[u][r].x : ks[u][r].y;
-                      dst[u][n][r] = fmaf(w & 1 ? bf16_high(sc) : bf16_low(sc), c[2 * r] + c[2 * r + 1], dst[u][n][r]);
-                    }
-                  } else {  // two groups, a step each
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                      float c[4];
-                      mma_f16_zero(c, {lo[0][e], lo[1][e], hi[0][e], hi[1][e]}, e ? q.z : q.x, e ? q.w : q.y);
-#pragma unroll
-                      for (int r = 0; r < 2; ++r) {
-                        const uint32_t sc = w == 0 ? ks[u][r].x : ks[u][r].y;
-                        dst[u][n][r] = fmaf(e ? bf16_high(sc) : bf16_low(sc), c[2 * r] + c[2 * r + 1], dst[u][n][r]);
-                      }
-                    }
-                  }
-                }
-              }
-          };
-          if (j <= jb) scores(std::true_type{}, s);
-          if (j + 16 * U - 1 > jb) {  // local keys, and the local ones where the window edge passes
-            float near[U][NQ][2];
-            scores(std::false_type{}, near);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
+        for (int u = 0; u <= U; ++u) {
+          float s[NQ][2];
+          if (u < U) scores(far_tag, u, s);
+          if (u > 0) values(u - 1);
+          if (u < U) weights(u, s, std::false_type{});
+        }
+      };
+
+      for (int tile = t0; tile < t1; ++tile) {
+        j = tile * T + wsub * 16 * U;
+        if (ok) ok = warp_wait(&sh.full[stage], phase, abort);
+        base = stages_at + stage * lay.stage;
+        JL_CHECK(tile < tiles && j >= 0 && L <= p.max_seqlen && head < HPB && hb * HPB + head < p.Hkv);
+        if (!ok) {
+        } else if (j + 16 * U <= L && j > jb) {
+          whole_tile(std::false_type{});
+        } else if (j + 16 * U <= L && j + 16 * U - 1 <= jb) {
+          whole_tile(std::true_type{});
+        } else {  // the window's edge or the entry's end
+#pragma unroll 1
+          for (int u = 0; u < U && j < L; ++u, j += 16) {
+            float s[NQ][2] = {}, near[NQ][2];
+            if (j <= jb) scores(std::true_type{}, u, s);
+            if (j + 15 > jb) {
+              scores(std::false_type{}, u, near);
 #pragma unroll
               for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                  s[u][n][r] = j + 16 * u + keyA + 8 * r <= jb ? s[u][n][r] : near[u][n][r];
-          }
-
-          // Weights and their products with the value scales.  M moves only when a product
-          // passes 2^14 (in the first keys: by anything), so it rarely does.
-          uint2 vs[U][2];
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) vs[u][r] = lds64(sa + u * next_scales + r * 128 * HPB + 8);
-          if (j + 16 * U > L) {  // keys behind the length: weight 0, and no NaN scale that it could meet
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-              for (int r = 0; r < 2; ++r)
-                if (j + 16 * u + keyA + 8 * r >= L) {
-                  vs[u][r] = make_uint2(0u, 0u);
-#pragma unroll
-                  for (int n = 0; n < NQ; ++n) s[u][n][r] = -INFINITY;
-                }
-            asm volatile("" ::: "memory");  // a branch: one tile of an entry takes it
-          }
-          float wt[U][NQ][2];
-          bool over = false;
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const uint2 v = vs[u][r];
-              const float top = fmaxf(fmax3(bf16_low(v.x), bf16_high(v.x), bf16_low(v.y)), fmaxf(bf16_high(v.y), 0x1p-90f));
-#pragma unroll
-              for (int n = 0; n < NQ; ++n) {
-                wt[u][n][r] = ex2_approx(fmaf(s[u][n][r], mul[n], -m[n]));
-                over |= wt[u][n][r] * top > 0x1p14f;
-              }
+                for (int r = 0; r < 2; ++r) s[n][r] = j + keyA + 8 * r <= jb ? s[n][r] : near[n][r];
             }
-          if (__any_sync(0xffffffffu, over)) {
-            float f[NQ];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-              float top = m[n] + 10.f;
-#pragma unroll
-              for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                  const uint2 v = vs[u][r];
-                  const float big = fmaxf(fmax3(bf16_low(v.x), bf16_high(v.x), bf16_low(v.y)), fmaxf(bf16_high(v.y), 0x1p-90f));
-                  top = fmaxf(top, fmaf(s[u][n][r], mul[n], __log2f(big)));
-                }
-#pragma unroll
-              for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-              const float now = top - 10.f;
-              f[n] = m[n] == -INFINITY ? 0.f : ex2_approx(m[n] - now);
-              m[n] = now;
-              l[n] *= f[n];
-#pragma unroll
-              for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) wt[u][n][r] = ex2_approx(fmaf(s[u][n][r], mul[n], -now));
-            }
-#pragma unroll
-            for (int n = 0; n < NP; ++n)
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const float by = f[NQ == 1 ? 0 : 2 * n + (y & 1)];
-#pragma unroll
-                for (int x = 0; x < MT; ++x) o[n][x][y] *= by;
-#pragma unroll
-                for (int x = 0; x < kF; ++x) eights[n][x][y] *= by;
-              }
-          }
-
-          // Values.  Column 2t of the weights is head t of score tile 2n, column 2t + 1 of
-          // tile 2n + 1; with one score tile both are head t, the even columns under the
-          // scales of the even groups and the odd ones under those of the odd groups.
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            uint32_t pf[NP][kF][2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float vf[4] = {bf16_low(vs[u][r].x), bf16_high(vs[u][r].x), bf16_low(vs[u][r].y), bf16_high(vs[u][r].y)};
-#pragma unroll
-              for (int n = 0; n < NQ; ++n) l[n] += wt[u][n][r];
-#pragma unroll
-              for (int n = 0; n < NP; ++n)
-#pragma unroll
-                for (int f = 0; f < kF; ++f) {
-                  const float a = wt[u][NQ == 1 ? 0 : 2 * n][r] * vf[NQ == 1 ? 2 * f : f];
-                  const float bb = wt[u][NQ == 1 ? 0 : 2 * n + 1][r] * vf[NQ == 1 ? 2 * f + 1 : f];
-                  pf[n][f][r] = transpose_8x8(h2_bits(__floats2half2_rn(a, bb)));
-                }
-            }
-            uint32_t vc[4][VW];  // value codes of keys key0, key1, key0 + 8, key1 + 8
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const uint32_t at = base + (r & 1 ? at_val1 : at_val0) + u * next_codes + (r >> 1) * eight;
-              if constexpr (D == 128) {
-                const uint2 v = lds64(at);
-                vc[r][0] = v.x, vc[r][1] = v.y;
-              } else {
-                vc[r][0] = lds32(at);
-              }
-            }
-#pragma unroll
-            for (int n = 0; n < NP; ++n)
-#pragma unroll
-              for (int f = 0; f < kF; ++f)
-                mma_f16(eights[n][f], {kEightsLow, kEightsHigh, kEightsLow, kEightsHigh}, pf[n][f][0], pf[n][f][1]);
-#pragma unroll
-            for (int w = 0; w < VW; ++w)
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const uint32_t pick = y ? 0x7632u : 0x5410u;
-                const uint32_t a = __byte_perm(vc[0][w], vc[1][w], pick), bb = __byte_perm(vc[2][w], vc[3][w], pick);
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {  // channel tile x: byte 2y + z of word w
-                  const int x = 4 * w + 2 * y + z, f = NQ == 1 ? x * 2 / MT : x * 4 / MT;
-                  const uint32_t az = a >> (8 * z), bz = bb >> (8 * z);
-                  const uint32_t frag[4] = {az & 0x000f000fu, az & 0x00f000f0u, bz & 0x000f000fu, bz & 0x00f000f0u};
-#pragma unroll
-                  for (int n = 0; n < NP; ++n) mma_f16(o[n][x], frag, pf[n][f][0], pf[n][f][1]);
-                }
-              }
+            weights(u, s, std::true_type{});
+            values(u);
           }
         }
         __syncwarp();

@@ -69,11 +69,6 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
                : "memory");
 }
 
-// Raises the bytes that the current phase waits for, without arriving.
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
-}
-
 // Tests the phase; if it is not complete the thread may be suspended until it
 // completes or until the time hint (ns) elapses, so a waiting warp does not
 // spin on the issue slots the working warps need.
