@@ -750,16 +750,16 @@ template <int D>
 jl_status dispatch_decode_q4(jl::DecodeQ4Params& prm, cudaStream_t st) {
   // Score tiles of four query heads (two columns each in an n = 8 matrix instruction); KV heads
   // of a block, which share its cos/sin rows, as many as eight key warps and 32 KB of query
-  // fragments allow; sixteens of keys of a warp in a tile.  Four hide more latency
-  // than two, and two more than one: at 128K keys of 128 channels 45.9 us against 50.5 for 32/8
-  // heads, and, two against one, 36.1 against 40.6 for 32/4.  A head block below eight has longer
-  // tiles, and four would leave it one stage of shared memory; so would two with eight query
-  // heads a KV head and a block of one (24/3 heads: 46.7 us against 39.1 with one).  Sixteen
-  // query heads leave no registers for two.
+  // fragments allow; sixteens of keys of a warp in a tile, as many as leave two stages of shared
+  // memory.  More hide more latency: at 128K keys of 128 channels (measured with half the cos/sin
+  // rows) 45.9 us with four against 50.5 with two for 32/8 heads, 36.8 with two against 40.6 with
+  // one for 32/4; one stage alone costs more than that (24/3 heads: 46.7 us with two sixteens in
+  // one stage, 39.1 with one in two).  Eight query heads leave registers for two, sixteen for one.
   const int nq = prm.group <= 4 ? 1 : prm.group <= 8 ? 2 : 4;
   int hpb = 8 / nq;
   while (prm.Hkv % hpb != 0) hpb /= 2;
-  const int sixteens = hpb == 8 ? 4 : nq == 1 || (nq == 2 && hpb > 1) ? 2 : 1;
+  int sixteens = 4 / nq;
+  while (sixteens > 1 && jl::decode_q4_layout(D, nq, hpb, 16 * sixteens * 8 / hpb).stages < 2) sixteens /= 2;
   prm.heads_per_block = hpb;
   prm.tile = 16 * sixteens * 8 / hpb;
   prm.tile_log2 = __builtin_ctz(prm.tile);
@@ -767,8 +767,13 @@ jl_status dispatch_decode_q4(jl::DecodeQ4Params& prm, cudaStream_t st) {
   if (tiles > 0x7fffffff) return fail(JL_ERR_UNSUPPORTED, "too many keys for one call (%lld tiles)", (long long)tiles);
   prm.n_cta = static_cast<int32_t>(std::min<int64_t>(jl::kDecodeQ4Ctas, tiles));
   if (nq == 4) return launch_decode_q4<D, 4, 1>(prm, st);
-  if (nq == 2) return sixteens == 2 ? launch_decode_q4<D, 2, 2>(prm, st) : launch_decode_q4<D, 2, 1>(prm, st);
-  return sixteens == 4 ? launch_decode_q4<D, 1, 4>(prm, st) : launch_decode_q4<D, 1, 2>(prm, st);
+  if constexpr (D == 128) {
+    if (nq == 2) return sixteens == 2 ? launch_decode_q4<D, 2, 2>(prm, st) : launch_decode_q4<D, 2, 1>(prm, st);
+    return sixteens == 2 ? launch_decode_q4<D, 1, 2>(prm, st) : launch_decode_q4<D, 1, 1>(prm, st);
+  } else {  // of 64 channels there is room for one more
+    if (nq == 2) return launch_decode_q4<D, 2, 2>(prm, st);
+    return sixteens == 4 ? launch_decode_q4<D, 1, 4>(prm, st) : launch_decode_q4<D, 1, 2>(prm, st);
+  }
 }
 
 jl_status decode_q4(jl::DecodeQ4Params prm, int32_t head_dim, float softmax_scale, void* workspace,

@@ -121,21 +121,22 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 //
 // What bounds it.  A row of 128 channels is 144 bytes: 128K keys of eight heads are 151 MB,
 // 23.0 us at the measured 6.56 TB/s.  Beside that stand, for 16 keys of one head (8192 of
-// those a head at 128K), some 360 warp instructions to expand, rotate, weigh and sum 4096
-// codes, 40 thousand a scheduler, of which the ALU and the fp16 pipe take two cycles each.
-// Measured (graph-replayed, 32/8 heads of 128, cold caches): 47.8 us at 128K keys (G = 4),
-// 3.2 TB/s, of which 37 us are per key and 10 for the start, the first loads and the join;
+// those a head at 128K), some 290 warp instructions to expand, weigh and sum 4096 codes and
+// 170 more to rotate the keys, of which the ALU and the fp16 pipe take two cycles each.
+// Measured (graph-replayed, 32/8 heads of 128, cold caches): 61.5 us at 128K keys (G = 4),
+// 2.5 TB/s, of which 52 us are per key and 9 for the start, the first loads and the join;
 // without rotation (G = 1) 28 us are per key.  8K keys take 10.4 us.  With the instructions
 // of the keys and values left out, the loads alone stream 128K keys in 21 us.  So the
-// arithmetic bounds it: issue slots are 58 % used, the ALU pipe 50 %, DRAM 48 %.
+// arithmetic bounds it: issue slots are 48 % used, the FMA pipe 45 %, DRAM 30 %.
 //
 // Shape.  Eight warps of a CTA take keys; one loads; three make the rotations' factors.  A
 // tile is `tile` keys of all KV heads of a head block: U sixteens of keys of one head for
 // each key warp.  It arrives by TMA as boxes of sixteen keys, in a ring of stages.  Two warps
-// a scheduler with U = 4 beat four of U = 1 with half the registers (51 against 61 us at
-// 128K): what a warp does once a tile costs as much as a third of its sixteen keys.  The values
-// of one sixteen stand beside the scores of the next, independent of them and on other pipes:
-// 45.9 us, against 47.8 with the scores of all four side by side, which keeps them apart.  For head blocks below eight, U = 2 keeps two stages in shared memory.
+// a scheduler with more sixteens a tile beat four of U = 1 with half the registers (51 against
+// 61 us at 128K, when the rotation had one rounding to fp16): what a warp does once a tile
+// costs as much as a third of its sixteen keys.  The values of one sixteen stand beside the
+// scores of the next, independent of them and on other pipes: 4 % less than with the scores
+// of all sixteens side by side, which keeps them apart.
 //
 // Matrix instructions: mma.m16n8k16 with the keys on M for the scores and the channels on M
 // for the values.  A lane expands the codes of its own fragments in registers.  tcgen05 would
@@ -147,10 +148,14 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 // scaled by a power of two to a largest channel in [8, 16) and split into two fp16 numbers,
 // columns 2h and 2h + 1 of B, which carry 22 of its bits (bf16 queries are exact, rotated
 // ones off by 2^-22).  Local keys therefore score exactly up to the fp32 sums.  A remote
-// key's pairs are first turned by R(f(j) - j) in fp16: cos and sin to 2^-12, one product
-// and one sum rounded to 11 bits, so a score is off by some 1e-4 of its size, more exact
-// than the bf16 keys of the 16-bit cache.  The group scales are applied to the fp32 sums of
-// their group, between the matrix instructions.
+// key's pairs are first turned by R(f(j) - j).  cos and sin are split into a multiple of 2^-7
+// and a remainder of at most 2^-8: the codes turned by the first are whole multiples of 2^-7
+// below 2^4, exact in fp16, and turned by the second they are so small that their rounding to
+// 11 bits is some 2^-19 of a code.  Both go through the matrix instruction against the same
+// query, so remote scores are as good as fp32 ones.  With cos, sin and the turned key rounded
+// to fp16 once, scores were off by 3e-4 of a key's part and the lse by 1.4e-6 of itself
+// (5e-8 now, the fp32 sums'); the remainders cost 15 us of the 61.5 at 128K keys.  The group
+// scales are applied to the fp32 sums of their group, between the matrix instructions.
 //
 // Weights are multiplied by the value scales of their key in fp32 and rounded to fp16 (2^-11
 // of each).  So that the products fit fp16 whatever the scales, the softmax's reference M is
@@ -160,8 +165,8 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 // share M, so it drops out.  Sums and outputs are held in fp32.
 //
 // The rotations' cos and sin are the same for all heads, so three warps make them once a tile
-// for the whole head block: from the table's row of the tile's first key by steps of one
-// position in fp32, stored as fp16 in the order of the fragments.
+// for the whole head block: from the table's row of a run's first key by steps of one position
+// in fp32, split as above and stored as fp16 in the order of the fragments.
 
 constexpr int kDecodeQ4Ctas = 148;  // one per SM
 constexpr int kDecodeQ4KeyWarps = 8, kDecodeQ4TurnWarps = 3, kDecodeQ4OtherWarps = 1 + kDecodeQ4TurnWarps;  // one loads
@@ -175,7 +180,7 @@ static_assert(kDecodeQ4KeyWarps * kDecodeQ4KeyRegs + kDecodeQ4OtherWarps * kDeco
               "the split has to fit the launch's registers, or setmaxnreg waits for good");
 
 // Shared memory: a region for the query fragments, reused to join the key warps, then the
-// stages.  A stage: key codes, value codes, scales, cos/sin rows.
+// stages.  A stage: key codes, value codes, scales, cos/sin rows, the rows' remainders.
 struct DecodeQ4Layout {
   int region, codes, scales, table, stage, stages, total;
 };
@@ -187,7 +192,7 @@ __host__ __device__ constexpr DecodeQ4Layout decode_q4_layout(int D, int NQ, int
   l.region = ((frags > join ? frags : join) + 1023) / 1024 * 1024;
   l.codes = tile * HPB * D / 2;
   l.scales = tile * HPB * 16;
-  l.table = tile * D * 2;
+  l.table = 2 * tile * D * 2;
   l.stage = 2 * l.codes + l.scales + l.table;
   l.stages = (220 * 1024 - l.region) / l.stage;
   if (l.stages > kDecodeQ4MaxStages) l.stages = kDecodeQ4MaxStages;
@@ -226,6 +231,11 @@ __device__ __forceinline__ void key_warps_sync() {
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+__device__ __forceinline__ uint32_t h2_of(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return h2_bits(__floats2half2_rn(a, b));
+}
 __device__ __forceinline__ uint32_t select_or(uint32_t x, uint32_t mask, uint32_t set) {
   uint32_t y;  // (x & mask) | set
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(mask), "r"(set));
@@ -240,6 +250,12 @@ __device__ __forceinline__ __half2 codes_f16(uint32_t w) {
     return __hfma2(bits_h2(select_or(w, 0x00f000f0u, 0x64006400u)), __float2half2_rn(0.0625f), __float2half2_rn(-72.f));
   else
     return __hsub2(bits_h2(select_or(w, 0x000f000fu, 0x64006400u)), __float2half2_rn(1032.f));
+}
+
+// A pair of channels (two keys' or two pairs' of them) turned back by the angle of cos c and sin s.
+__device__ __forceinline__ void turn_pair(__half2 a, __half2 b, uint32_t c, uint32_t s, uint32_t& x, uint32_t& y) {
+  x = h2_bits(__hfma2(a, bits_h2(c), __hmul2(b, bits_h2(s))));
+  y = h2_bits(__hfma2(b, bits_h2(c), __hneg2(__hmul2(a, bits_h2(s)))));
 }
 
 // Value codes are fed as they are: four bits at the bottom of an fp16 are the subnormal
@@ -401,23 +417,25 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
       return;
     }
     // ------------------------------------------------------------ cos/sin rows --
-    // Each warp makes a third of a tile's rows: from the tables' row of its first key (row
-    // j - floor(j / G)), asked for a tile ahead, by one position's step after the other in fp32
-    // (at most 88 steps: an error of some 2^-17 before the rounding to fp16).  Eight keys at a
-    // time, each from a row of its own asked for eight keys ahead, took 27 us for 128K keys, the
-    // rows' latency; one warp for all of a tile's rows took 43.
+    // Each warp makes a third of a tile's rows (half a warp a sixth, of 64 channels): from the
+    // tables' row of its first key (row j - floor(j / G)), asked for a tile ahead, by one
+    // position's step after the other in fp32 (at most 44 steps: an error of some 2^-18).
+    // Eight keys at a time, each from a row of its own asked for eight keys ahead, took 27 us
+    // for 128K keys, the rows' latency; one warp for all of a tile's rows took 43.
     const int tw = warp - kDecodeQ4KeyWarps - 1;
     // lane -> the two pairs of one packed register: word w, fragment lane t, register half e
-    const bool has = D == 128 || lane < 16;
-    const int w = D == 128 ? lane / 8 : (lane & 15) / 8, t = D == 128 ? (lane / 2) & 3 : lane & 3;
-    const int e = D == 128 ? lane & 1 : (lane >> 2) & 1;
+    const int w = D == 128 ? lane / 8 : (lane & 15) / 8, t = (lane / 2) & 3, e = lane & 1;
     const int c0 = D == 128 ? 16 * w + 4 * t + e : 8 * (2 * w + e) + 2 * t, c1 = D == 128 ? c0 + 2 : c0 + 1;
     // one position's step of both pairs, packed; with a table of one row nothing is remote
     const int64_t one = p.n_tab_rows > 1 ? HALF : 0;
     const uint64_t step_c = f2_pack(p.cos_tab[one + c0], p.cos_tab[one + c1]);
     const uint64_t step_s = f2_pack(p.sin_tab[one + c0], p.sin_tab[one + c1]);
     const uint64_t step_n = f2_pack(-p.sin_tab[one + c0], -p.sin_tab[one + c1]);
-    const int row0 = T / 8 * tw / kDecodeQ4TurnWarps * 8, row1 = T / 8 * (tw + 1) / kDecodeQ4TurnWarps * 8;
+    constexpr int kRuns = kDecodeQ4TurnWarps * 128 / D;  // runs of rows: half a warp does one of 64 channels
+    const int run = D == 128 ? tw : 2 * tw + lane / 16;
+    const int row0 = T / 4 * run / kRuns * 4, row1 = T / 4 * (run + 1) / kRuns * 4;
+    const int rest = lay.table / 2;  // the remainders' rows, behind the others
+    const uint64_t grid = f2_pack(98304.f, 98304.f);  // 1.5 * 2^16: a sum with it ends at 2^-7
     while (cur < st.end && ok) {
       const int tiles = q4_tiles(p, L);
       const int t1 = min(tiles, t0 + (st.end - cur));
@@ -446,29 +464,24 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
           if (tile + 1 < far_tiles) ask((tile + 1) * T + row0);
           // even and odd rows from two places, so that the offsets in the loop are constants
           uint8_t* const rows = stages + stage * lay.stage + 2 * lay.codes + lay.scales + row0 * 2 * D;
-          uint8_t* even = rows + q4_turn_at<D>(0, w, t) + 4 * e;
-          uint8_t* odd = rows + q4_turn_at<D>(1, w, t) + 4 * e - 2 * D;
-          for (int r = row0; r < row1; r += 8) {
+          uint8_t* even = rows + q4_turn_at<D>(0, w, t) + 8 * e;
+          uint8_t* odd = rows + q4_turn_at<D>(1, w, t) + 8 * e - 2 * D;
+          for (int r = row0; r < row1; r += 4) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
+            for (int x = 0; x < 4; ++x) {
               uint8_t* at = (x & 1 ? odd : even) + x * 2 * D;
-              float c[2], sn[2];
-              f2_unpack(ac, c[0], c[1]);
-              f2_unpack(as, sn[0], sn[1]);
-              if (has) {
-                *reinterpret_cast<__half2*>(at) = __floats2half2_rn(c[0], c[1]);
-                *reinterpret_cast<__half2*>(at + 8) = __floats2half2_rn(sn[0], sn[1]);
-              }
-              if (--left == 0) {
-                left = grow;
-              } else {
-                const uint64_t nc = f2_fma(ac, step_c, f2_mul(as, step_n));
-                as = f2_fma(as, step_c, f2_mul(ac, step_s));
-                ac = nc;
-              }
+              const uint64_t gc = f2_sub(f2_add(ac, grid), grid), gs = f2_sub(f2_add(as, grid), grid);
+              *reinterpret_cast<uint2*>(at) = make_uint2(h2_of(gc), h2_of(gs));
+              *reinterpret_cast<uint2*>(at + rest) = make_uint2(h2_of(f2_sub(ac, gc)), h2_of(f2_sub(as, gs)));
+              // no branch, so that the next rows' steps fill the waits of this one's
+              const uint64_t nc = f2_fma(ac, step_c, f2_mul(as, step_n)), ns = f2_fma(as, step_c, f2_mul(ac, step_s));
+              const bool stay = --left == 0;
+              ac = stay ? ac : nc;
+              as = stay ? as : ns;
+              left = stay ? grow : left;
             }
-            even += 16 * D;
-            odd += 16 * D;
+            even += 8 * D;
+            odd += 8 * D;
           }
         }
         __syncwarp();
@@ -637,27 +650,29 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
         for (int n = 0; n < NQ; ++n) dst[n][0] = dst[n][1] = 0.f;
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-          uint4 turn[2];
-          if constexpr (FAR) {
-            turn[0] = lds128((w & 1 ? turn1 : turn0) + (w >> 1) * 128);
-            turn[1] = lds128((w & 1 ? turn1 : turn0) + (w >> 1) * 128 + 16 * D);
-          }
-          uint32_t lo[2][2], hi[2][2];  // [row][register half]
+          uint32_t lo[2][2], hi[2][2];    // [row][register half]
+          uint32_t rlo[2][2], rhi[2][2];  // far: what the remainders of cos and sin add
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
+          for (int r = 0; r < 2; ++r) {
+            uint4 turn, rest;
+            if constexpr (FAR) {
+              const uint32_t at = (w & 1 ? turn1 : turn0) + (w >> 1) * 128 + r * 16 * D;
+              turn = lds128(at);
+              rest = lds128(at + lay.table / 2);
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const uint32_t word = e ? kc[r][w] >> 8 : kc[r][w];
-              __half2 a = codes_f16<false>(word), bb = codes_f16<true>(word);
+              const __half2 a = codes_f16<false>(word), bb = codes_f16<true>(word);
               if constexpr (FAR) {  // R(-n)
-                const __half2 c = bits_h2(e ? turn[r].y : turn[r].x), sn = bits_h2(e ? turn[r].w : turn[r].z);
-                const __half2 na = __hfma2(a, c, __hmul2(bb, sn));
-                bb = __hfma2(bb, c, __hneg2(__hmul2(a, sn)));
-                a = na;
+                turn_pair(a, bb, e ? turn.z : turn.x, e ? turn.w : turn.y, lo[r][e], hi[r][e]);
+                turn_pair(a, bb, e ? rest.z : rest.x, e ? rest.w : rest.y, rlo[r][e], rhi[r][e]);
+              } else {
+                lo[r][e] = h2_bits(a);
+                hi[r][e] = h2_bits(bb);
               }
-              lo[r][e] = h2_bits(a);
-              hi[r][e] = h2_bits(bb);
             }
+          }
 #pragma unroll
           for (int n = 0; n < NQ; ++n) {
             uint4 q;
@@ -667,6 +682,10 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
               float c[4];
               mma_f16_zero(c, {lo[0][0], lo[1][0], lo[0][1], lo[1][1]}, q.x, q.y);
               mma_f16(c, {hi[0][0], hi[1][0], hi[0][1], hi[1][1]}, q.z, q.w);
+              if constexpr (FAR) {
+                mma_f16(c, {rlo[0][0], rlo[1][0], rlo[0][1], rlo[1][1]}, q.x, q.y);
+                mma_f16(c, {rhi[0][0], rhi[1][0], rhi[0][1], rhi[1][1]}, q.z, q.w);
+              }
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
                 const uint32_t sc = w < 2 ? ks[r].x : ks[r].y;
@@ -677,6 +696,8 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
               for (int e = 0; e < 2; ++e) {
                 float c[4];
                 mma_f16_zero(c, {lo[0][e], lo[1][e], hi[0][e], hi[1][e]}, e ? q.z : q.x, e ? q.w : q.y);
+                if constexpr (FAR)
+                  mma_f16(c, {rlo[0][e], rlo[1][e], rhi[0][e], rhi[1][e]}, e ? q.z : q.x, e ? q.w : q.y);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                   const uint32_t sc = w == 0 ? ks[r].x : ks[r].y;

@@ -2,10 +2,9 @@
 against the definition in 64 bits, and all of them together as a user calls them.
 
 Decode tolerances are the framework's own for a decode (out max-abs 2e-2 and mean-abs 2e-3 for values
-of unit variance, lse 1e-2).  They cover the two roundings that are the kernel's own: a rotated key
-component is off by at most 2^-8 + 2^-9 + 14 * 2^-12 code steps (its fp16 result, its first product, the
-fp16 cos and sin), at a step of 0.4 and independent over 128 channels a score error of about 1e-3; and
-the weights of the value product carry bf16's 2^-8, which averages over the keys."""
+of unit variance, lse 1e-2).  The one rounding of the kernel that shows in them is that of the weights
+times the value scales to fp16, 2^-12 of each, which averages over the keys; the lse, which it does not
+touch, has a test of its own."""
 import numpy as np
 import pytest
 import torch
@@ -468,8 +467,23 @@ def test_a_long_cache(jl, d, hq, hkv):
     jl.jl_sync_status()
     want = expect(q, cache, [L], 4096, 32768)
     close(out, lse, want)
-    # score errors of 1e-3 and less, independent over some thousand keys that share the weight
     assert np.abs(R.f32(lse) - want[1]).max() <= 1e-4
+
+
+@pytest.mark.parametrize("d,hq,hkv", SHAPES + [(64, 12, 2), (64, 8, 1), (64, 16, 1), (64, 32, 2), (128, 32, 2), (128, 15, 3)])
+def test_remote_scores_are_as_good_as_fp32(jl, d, hq, hkv):
+    """A turned component is off by the 44 steps of its cos and sin, 14 * 44 * 2^-24 code steps, and by its
+    remainder's three roundings, 3 * 14 * 2^-8 * 2^-12: 7.7e-5 at the most, at a step of 0.4 and independent over
+    the channels a score error of 2e-5 (1e-5 in the mean square of evenly spread ones); the lse averages that over
+    the keys.  Keys turned in one fp16 number are off by 2^-8 code steps and more, fifty times that."""
+    lens = (700, 2048)
+    cache = random_cache(71, len(lens), 2048, hkv, d)
+    q = normal(72, len(lens), hq, d)
+    cos, sin = tables(2048, d)
+    _, lse = jl.jl_bifocal_decode_q4(q, *cache, dev(lens, torch.int32), 2048, 0, 500, cos, sin)
+    jl.jl_sync_status()
+    want = expect(q, cache, lens, 0, 500)
+    assert np.abs(R.f32(lse) - want[1]).max() <= 2e-5
 
 
 def test_rows_past_two_gigabytes(jl):
