@@ -64,6 +64,16 @@ def build_last_cta(force: bool = False) -> str:
     return build(force=force, extra=["-DJL_DECODE_LAST_CTA_MERGE=1"], out=LAST_CTA_LIB)
 
 
+# The time-out test build: a cos/sin warp of the 4-bit decode gives up at its CTA's fourth tile
+# (-DJL_Q4_GIVE_UP=3), and a bounded wait ends after some 2 ms.
+GIVE_UP_LIB = os.path.join(HERE, "libjetlong_giveup.so")
+
+
+def build_give_up(force: bool = False) -> str:
+    """Build libjetlong_giveup.so (a 4-bit decode that gives up) in-tree."""
+    return build(force=force, extra=["-DJL_Q4_GIVE_UP=3", "-DJL_WAIT_LIMIT_CYCLES=4000000ll"], out=GIVE_UP_LIB)
+
+
 if __name__ == "__main__":
     build(force=True, verbose=True, extra=sys.argv[1:])
     print(LIB)

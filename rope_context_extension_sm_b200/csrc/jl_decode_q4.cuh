@@ -173,6 +173,13 @@ constexpr int kDecodeQ4KeyWarps = 8, kDecodeQ4TurnWarps = 3, kDecodeQ4OtherWarps
 constexpr int kDecodeQ4Threads = 32 * (kDecodeQ4KeyWarps + kDecodeQ4OtherWarps);
 constexpr int kDecodeQ4MaxStages = 6;
 
+// Test build of the time-outs: one of every CTA's cos/sin warps gives up at its tile of this number.
+#ifdef JL_Q4_GIVE_UP
+constexpr int kDecodeQ4GiveUp = JL_Q4_GIVE_UP;
+#else
+constexpr int kDecodeQ4GiveUp = -1;
+#endif
+
 // Registers a thread: 168 at launch; the key warps rise to 216, the others drop to 72.
 constexpr int kDecodeQ4Regs = 168, kDecodeQ4KeyRegs = 216, kDecodeQ4OtherRegs = 72;
 static_assert(kDecodeQ4KeyWarps * kDecodeQ4KeyRegs + kDecodeQ4OtherWarps * kDecodeQ4OtherRegs <=
@@ -202,11 +209,12 @@ __host__ __device__ constexpr DecodeQ4Layout decode_q4_layout(int D, int NQ, int
 
 struct DecodeQ4Shared {
   uint64_t full[kDecodeQ4MaxStages];   // codes and scales have arrived, cos/sin rows are written
-  uint64_t empty[kDecodeQ4MaxStages];
+  uint64_t empty[kDecodeQ4MaxStages];  // all key warps are done with the stage; one that gave up frees none
   float mul[32];                       // log2 units per unit of score, by query head of the block
   float red_m[kDecodeQ4KeyWarps][16], red_l[kDecodeQ4KeyWarps][16];
   Q4Start start;
   int abort;
+  int issued;  // tiles that the load warp asked for, once it will ask for no more; -1 before
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -333,6 +341,7 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
       mbar_init(&sh.empty[s], kDecodeQ4KeyWarps);
     }
     sh.abort = 0;
+    sh.issued = -1;
     fence_mbar_init();
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
@@ -409,8 +418,11 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
         }
         if (cur < st.end) L = p.seqlens[b];
       }
-      if (!ok && lane == 0) {
-        // gave up: the copies in flight land before the block leaves its shared memory
+      // Drain: never leave the block with a copy still landing in its shared memory.  A stage is
+      // loaded again only after all key warps saw its last load, so these tiles' copies are the only
+      // ones in flight; `full` completes for each, as a cos/sin warp that gives up arrives for it too.
+      if (lane == 0) {
+        *static_cast<volatile int*>(&sh.issued) = issued;
         for (int x = max(0, issued - lay.stages); x < issued; ++x)
           mbar_wait_bounded(&sh.full[x % lay.stages], (x / lay.stages) & 1);
       }
@@ -436,6 +448,7 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
     const int row0 = T / 4 * run / kRuns * 4, row1 = T / 4 * (run + 1) / kRuns * 4;
     const int rest = lay.table / 2;  // the remainders' rows, behind the others
     const uint64_t grid = f2_pack(98304.f, 98304.f);  // 1.5 * 2^16: a sum with it ends at 2^-7
+    int made = 0;  // tiles that this warp arrived for, where it gave up
     while (cur < st.end && ok) {
       const int tiles = q4_tiles(p, L);
       const int t1 = min(tiles, t0 + (st.end - cur));
@@ -454,8 +467,10 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
       };
       if (t0 < far_tiles) ask(t0 * T + row0);
       for (int tile = t0; tile < t1; ++tile) {
-        if (!warp_wait(&sh.empty[stage], phase ^ 1, abort)) {
+        if (!warp_wait(&sh.empty[stage], phase ^ 1, abort) ||
+            (kDecodeQ4GiveUp >= 0 && tw == 0 && cur - st.begin + tile - t0 == kDecodeQ4GiveUp)) {
           ok = false;
+          made = cur - st.begin + tile - t0;
           break;
         }
         if (tile < far_tiles) {
@@ -498,6 +513,17 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
         ++hb;
       }
       if (cur < st.end) L = p.seqlens[b];
+    }
+    if (!ok && lane == 0) {
+      // Gave up: tiles that were asked for complete `full` all the same, for the load warp's drain.
+      // That warp's waits end, its own limit or the abort flag being seen, within one limit.
+      *abort = 1;
+      atomicOr(&g_status, kDevErrTimeout);
+      const volatile int* issued = &sh.issued;
+      const long long since = clock64();
+      while (*issued < 0 && clock64() - since < 2 * JL_WAIT_LIMIT_CYCLES) {
+      }
+      for (int x = made; x < *issued; ++x) mbar_arrive(&sh.full[x % lay.stages]);
     }
     return;
   }
@@ -856,7 +882,7 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[stage]);
+        if (lane == 0 && ok) mbar_arrive(&sh.empty[stage]);
         if (++stage == lay.stages) {
           stage = 0;
           phase ^= 1;
