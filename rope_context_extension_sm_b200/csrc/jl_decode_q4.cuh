@@ -157,8 +157,10 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 // (5e-8 now, the fp32 sums'); the remainders cost 15 us of the 61.5 at 128K keys.  The group
 // scales are applied to the fp32 sums of their group, between the matrix instructions.
 //
-// Weights are multiplied by the value scales of their key in fp32 and rounded to fp16 (2^-11
-// of each).  So that the products fit fp16 whatever the scales, the softmax's reference M is
+// Weights are multiplied by the value scales of their key in fp32 and rounded to fp16 (2^-11 of
+// each), three bits more than the bf16 of the cached values' scales and of the output: the output
+// is off by 2.0e-4 of its size from it at every length, beside 1.67e-3 of its own rounding.  A second
+// fp16 number for the rest would double the values' matrix instructions.  So that the products fit fp16 whatever the scales, the softmax's reference M is
 // not the largest score but follows the largest score + log2(largest scale of the key): M
 // keeps weight * scale = 2^(score - M) * scale at or below 2^14, where it was 2^10 when M last
 // moved, and products down to 2^-34 of the largest still count.  Numerator and denominator
@@ -266,12 +268,19 @@ __device__ __forceinline__ void turn_pair(__half2 a, __half2 b, uint32_t c, uint
   y = h2_bits(__hfma2(b, bits_h2(c), __hneg2(__hmul2(a, bits_h2(s)))));
 }
 
-// Value codes are fed as they are: four bits at the bottom of an fp16 are the subnormal
-// n 2^-24, in the high four bits of its byte n 2^-20, both exact operands of the matrix
-// instruction.  The 8 that every code is over is taken off at the end, 8 times the sum of
-// the weights as the matrix instruction sums them (kEights is 8 in both units); against sums
-// of codes of 0 .. 15 that loses no more than a bit.
-constexpr uint32_t kEightsLow = 0x00080008u, kEightsHigh = 0x00800080u;
+// The same for the value codes, the high four bits' in units of 1/16 (taken off at the end).
+// The 8 goes off the operands although codes of 0 .. 15, as fp16 subnormals, would need no
+// arithmetic and 8 times the sum of the weights could be taken off the sums (1 us less at 128K
+// keys): the matrix instruction cuts every product and the sum towards zero, two bits and none
+// below the last place of its largest operand.  Signed products are cut to either side, and the
+// running sum is no larger than the result; sums of positive ones are all cut one way, by more
+// the longer they grow.  The result was off by 4e-4 of itself at 886 keys a warp and by 7e-3 at
+// 8192, where signed ones are off by what the weights' rounding gives at every length.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t value_codes_f16(uint32_t w) {
+  const uint32_t x = HIGH ? select_or(w, 0x00f000f0u, 0x64006400u) : select_or(w, 0x000f000fu, 0x64006400u);
+  return h2_bits(__hsub2(bits_h2(x), __float2half2_rn(HIGH ? 1152.f : 1032.f)));
+}
 
 __device__ __forceinline__ void prefetch_l2(const void* x) { asm volatile("prefetch.global.L2 [%0];" ::"l"(x)); }
 
@@ -622,7 +631,7 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
       }
       key_warps_sync();
 
-      float o[NP][MT][4], eights[NP][kF][4], m[NQ], l[NQ], mul[NQ];
+      float o[NP][MT][4], m[NQ], l[NQ], mul[NQ];
       uint4 qf[kQueryRegs ? NQ * KW : 1];
       int have = -1;  // the variant that qf holds
 #pragma unroll
@@ -634,12 +643,9 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
 #pragma unroll
       for (int n = 0; n < NP; ++n)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
+        for (int y = 0; y < 4; ++y)
 #pragma unroll
           for (int x = 0; x < MT; ++x) o[n][x][y] = 0.f;
-#pragma unroll
-          for (int f = 0; f < kF; ++f) eights[n][f][y] = 0.f;
-        }
 
       uint32_t base = 0;         // the stage's address
       int j = 0;                 // first key of the sixteen at hand
@@ -787,8 +793,6 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
               const float by = f[NQ == 1 ? 0 : 2 * n + (y & 1)];
 #pragma unroll
               for (int x = 0; x < MT; ++x) o[n][x][y] *= by;
-#pragma unroll
-              for (int x = 0; x < kF; ++x) eights[n][x][y] *= by;
             }
         }
         // Column 2t of the weights is head t of score tile 2n, column 2t + 1 of tile 2n + 1; with
@@ -822,11 +826,6 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
           }
         }
 #pragma unroll
-        for (int n = 0; n < NP; ++n)
-#pragma unroll
-          for (int f = 0; f < kF; ++f)
-            mma_f16(eights[n][f], {kEightsLow, kEightsHigh, kEightsLow, kEightsHigh}, pf[n][f][0], pf[n][f][1]);
-#pragma unroll
         for (int w = 0; w < VW; ++w)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
@@ -836,7 +835,8 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
             for (int z = 0; z < 2; ++z) {  // channel tile x: byte 2y + z of word w
               const int x = 4 * w + 2 * y + z, f = NQ == 1 ? x * 2 / MT : x * 4 / MT;
               const uint32_t az = a >> (8 * z), bz = bb >> (8 * z);
-              const uint32_t frag[4] = {az & 0x000f000fu, az & 0x00f000f0u, bz & 0x000f000fu, bz & 0x00f000f0u};
+              const uint32_t frag[4] = {value_codes_f16<false>(az), value_codes_f16<true>(az), value_codes_f16<false>(bz),
+                                        value_codes_f16<true>(bz)};
 #pragma unroll
               for (int n = 0; n < NP; ++n) mma_f16(o[n][x], frag, pf[n][f][0], pf[n][f][1]);
             }
@@ -908,9 +908,8 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
           const float inv = 1.f / l[n];
 #pragma unroll
           for (int x = 0; x < MT; ++x) {
-            const int y = NQ == 1 ? (x * 4 / MT) & 1 : n & 1, f = NQ == 1 ? x * 2 / MT : x * 4 / MT;
-            const float lo = (o[n / 2][x][y] - eights[n / 2][f][y]) * 0x1p24f;
-            const float hi = (o[n / 2][x][2 + y] - eights[n / 2][f][2 + y]) * 0x1p20f;
+            const int y = NQ == 1 ? (x * 4 / MT) & 1 : n & 1;
+            const float lo = o[n / 2][x][y], hi = o[n / 2][x][2 + y] * 0.0625f;
             if (whole) {
               p.out[at * D + 16 * x + g] = __float2bfloat16_rn(lo * inv);
               p.out[at * D + 16 * x + 8 + g] = __float2bfloat16_rn(hi * inv);
@@ -936,9 +935,8 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
 #pragma unroll
         for (int x = 0; x < MT; ++x) {
           const int y = NQ == 1 ? (x * 4 / MT) & 1 : n & 1;  // the column that holds this head under this group's scales
-          const int f = NQ == 1 ? x * 2 / MT : x * 4 / MT;
-          row[16 * x] = (o[n / 2][x][y] - eights[n / 2][f][y]) * 0x1p24f;
-          row[16 * x + 8] = (o[n / 2][x][2 + y] - eights[n / 2][f][2 + y]) * 0x1p20f;
+          row[16 * x] = o[n / 2][x][y];
+          row[16 * x + 8] = o[n / 2][x][2 + y] * 0.0625f;
         }
       }
       key_warps_sync();

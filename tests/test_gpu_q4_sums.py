@@ -1,0 +1,150 @@
+"""The sums of the 4-bit decode by themselves: the values' sums over many keys of one warp, where the result is
+a small difference, and outputs of long caches relative to their own size."""
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_q4 as Q
+from test_gpu_q4 import jl  # noqa: F401  (the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def uniform_codes(g, *shape):
+    n = lambda: torch.randint(1, 16, shape, generator=g, device="cuda", dtype=torch.uint8)  # noqa: E731
+    return n() | n() << 4
+
+
+def value_rows(v_codes, scales):
+    """The fp32 values of rows [..][d/2], [..][8], on the GPU."""
+    d = 2 * v_codes.shape[-1]
+    place = [Q.R.value_place(d, c) for c in range(d)]
+    byte = torch.tensor([b for b, _ in place], device="cuda")
+    shift = torch.tensor([s for _, s in place], device="cuda", dtype=torch.uint8)
+    group = torch.tensor([4 + Q.R.value_group(d, c) for c in range(d)], device="cuda")
+    return ((v_codes[..., byte] >> shift) & 15).float().sub_(8).mul_(scales.float()[..., group])
+
+
+def key_rows(k_codes, scales):
+    d = 2 * k_codes.shape[-1]
+    place = [Q.R.key_place(d, c) for c in range(d)]
+    byte = torch.tensor([b for b, _ in place], device="cuda")
+    shift = torch.tensor([s for _, s in place], device="cuda", dtype=torch.uint8)
+    group = torch.tensor([Q.R.key_group(d, c) for c in range(d)], device="cuda")
+    return ((k_codes[..., byte] >> shift) & 15).float().sub_(8).mul_(scales.float()[..., group])
+
+
+def rope64(x, pos):
+    """R(pos) x, rows x [n][..][d] in 64 bits, pos [n]."""
+    h = x.shape[-1] // 2
+    ang = pos.double()[:, None] * Q.BASE ** (-2.0 * torch.arange(h, device="cuda", dtype=torch.float64) / (2 * h))
+    z = torch.complex(x[..., :h], x[..., h:]) * torch.polar(torch.ones_like(ang), ang).unflatten(0, (-1, *[1] * (x.dim() - 2)))
+    return torch.cat([z.real, z.imag], -1)
+
+
+def expect_gpu(q, cache, L, w0, w_pre):
+    """The definition in 64 bits on the GPU: q [hq][d], cache rows [stride][hkv][..] of one entry -> out, lse."""
+    k, v = key_rows(cache[0][:L], cache[2][:L]).double(), value_rows(cache[1][:L], cache[2][:L]).double()
+    grow, i = max(1, -(-L // w_pre)), L - 1
+    edge = max(0, min(L, i - w0 + 1)) if grow > 1 else 0  # keys before it are remote
+    j = torch.arange(edge, device="cuda")
+    k[:edge] = rope64(k[:edge], j // grow - j)
+    near = q.double()
+    far = rope64(near[None], torch.tensor([i // grow - i], device="cuda"))[0]
+    kv = torch.arange(q.shape[0], device="cuda") // (q.shape[0] // k.shape[1])
+    k, v = k.transpose(0, 1)[kv], v.transpose(0, 1)[kv]  # [hq][L][d]
+    s = torch.cat([(k[:, :edge] @ far[:, :, None]), (k[:, edge:] @ near[:, :, None])], 1)[..., 0] / q.shape[1] ** 0.5
+    return (torch.softmax(s, -1)[:, None] @ v)[:, 0], torch.logsumexp(s, -1)
+
+
+def excess(out, want):
+    """How far a bf16 result is off beyond its own rounding (half a step of the wanted value's binade), as a
+    share of the root mean square of its head's wanted values."""
+    want = want.double()
+    step = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=2.0**-120))))
+    over = (out.double() - want).abs() - 2.0**-8 * step
+    return (over / want.square().mean(-1, keepdim=True).sqrt()).max().item()
+
+
+# (B, L, hq, hkv, d): one entry over all CTAs; one entry a CTA, all of its keys in eight warps, or in one
+MANY = [(1, 131072, 32, 8, 128), (148, 65536, 1, 1, 64), (150, 20000, 4, 1, 128), (148, 16384, 16, 1, 128),
+        (148, 8192, 8, 8, 64), (149, 9000, 10, 2, 128)]
+
+
+@pytest.mark.parametrize("B,L,hq,hkv,d", MANY)
+def test_values_that_cancel_leave_nothing(jl, B, L, hq, hkv, d):  # noqa: F811
+    """Equal weights, keys 2n and 2n + 1 with opposite values, so the result is 0.  While the sums that the kernel
+    holds stay below 2^9 weights, an instruction that is off by a last place two bits above fp32's is off by 2^-22
+    of that: 2^-13 of a weight for sixteen keys, if always to one side 2^-17 of a value's step.  The weights' sum is
+    one of L / 16 equal terms a lane and head at the most, each addition off by half a last place, 2^-24."""
+    g = torch.Generator(device="cuda").manual_seed(91)
+    vc = uniform_codes(g, B, L // 2, 1, hkv, d // 2).expand(B, L // 2, 2, hkv, d // 2).clone()
+    low, high = vc[:, :, 1] & 15, vc[:, :, 1] >> 4
+    vc[:, :, 1] = (16 - low) | (16 - high) << 4
+    sc = torch.empty(B, L // 2, 1, hkv, 8, device="cuda").uniform_(0.15, 0.31, generator=g).bfloat16()
+    sc = sc.expand(B, L // 2, 2, hkv, 8).clone()
+    vc, sc, kc = vc.flatten(1, 2), sc.flatten(1, 2), uniform_codes(g, B, L, hkv, d // 2)
+    tab = torch.ones(L, d // 2, device="cuda")
+    q = torch.zeros(B, hq, d, dtype=torch.bfloat16, device="cuda")
+    out, lse = jl.jl_bifocal_decode_q4(q, kc, vc, sc, Q.dev([L] * B, torch.int32), L, 0, L, tab, tab)
+    jl.jl_sync_status()
+    assert out.float().abs().max().item() <= 0.31 * 2.0**-17
+    assert (lse - np.log(L)).abs().max().item() <= 2.0**-20 * np.log(L) + 2.0**-24 * L / 16
+
+
+@pytest.mark.parametrize("B,L,hq,hkv,d", MANY)
+def test_mean_of_many_values(jl, B, L, hq, hkv, d):  # noqa: F811
+    """Equal weights: their products with a bf16 scale are exact in fp16, so what is left beside the output's
+    rounding is that of the sums, which are of the size of the result: a thousandth of it covers 2^13 roundings of
+    2^-23 all to one side."""
+    g = torch.Generator(device="cuda").manual_seed(92)
+    kc, vc = uniform_codes(g, B, L, hkv, d // 2), uniform_codes(g, B, L, hkv, d // 2)
+    sc = torch.empty(B, L, hkv, 8, device="cuda").uniform_(0.15, 0.31, generator=g).bfloat16()
+    tab = torch.ones(L, d // 2, device="cuda")
+    q = torch.zeros(B, hq, d, dtype=torch.bfloat16, device="cuda")
+    out, _ = jl.jl_bifocal_decode_q4(q, kc, vc, sc, Q.dev([L] * B, torch.int32), L, 0, L, tab, tab)
+    jl.jl_sync_status()
+    for b in (0, B // 2, B - 1):
+        want = value_rows(vc[b], sc[b]).double().mean(0).repeat_interleave(hq // hkv, 0)
+        assert excess(out[b], want) <= 1e-3
+
+
+@pytest.mark.parametrize("B,L,hq,hkv,d", [(148, 65536, 1, 1, 64), (150, 20000, 4, 1, 128), (148, 16384, 8, 8, 64),
+                                          (148, 16384, 16, 1, 128), (149, 9000, 10, 2, 128)])
+def test_many_keys_a_warp_relative_to_their_size(jl, B, L, hq, hkv, d):  # noqa: F811
+    """Batches that leave a warp up to 16384 keys, values quantised from a normal distribution.  Weights rounded
+    to fp16 as in the test below: six deviations of 2^-11 / sqrt(3).  An instruction for sixteen keys may cut the
+    running sum by its last place, 2^-23 of it, to one side: 2^-13 after a warp's 1024 of them."""
+    g = torch.Generator(device="cuda").manual_seed(96)
+    kc = uniform_codes(g, B, L, hkv, d // 2)
+    vc, sc = torch.empty_like(kc), torch.empty(B, L, hkv, 8, dtype=torch.bfloat16, device="cuda")
+    tab = torch.ones(L, d // 2, device="cuda")
+    for b in range(B):  # the values as the writer quantises them
+        v = torch.randn(L, hkv, d, generator=g, device="cuda").bfloat16()
+        spare = torch.empty(1, L, hkv, d // 2, dtype=torch.uint8, device="cuda")
+        jl.jl_kv_cache_fill_q4(v, v, Q.dev([0, L], torch.int32), tab, tab * 0, spare, vc[b:b + 1], sc[b:b + 1])
+    sc[..., :4].uniform_(0.15, 0.31, generator=g)
+    q = torch.randn(B, hq, d, generator=g, device="cuda").bfloat16()
+    out, lse = jl.jl_bifocal_decode_q4(q, kc, vc, sc, Q.dev([L] * B, torch.int32), L, 0, L, tab, tab)
+    jl.jl_sync_status()
+    for b in (0, B // 2, B - 1):
+        want, want_lse = expect_gpu(q[b], (kc[b], vc[b], sc[b]), L, 0, L)
+        assert excess(out[b], want) <= 6 * 2.0**-11 / 3**0.5 + 2.0**-13
+        assert (lse[b] - want_lse).abs().max().item() <= 2e-5
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(128, 32, 8), (128, 16, 8), (64, 16, 4), (128, 20, 5), (128, 16, 1), (64, 8, 1)])
+@pytest.mark.parametrize("w0,w_pre", [(4096, 32768), (0, 1 << 20)])
+def test_long_outputs_relative_to_their_size(jl, d, hq, hkv, w0, w_pre):  # noqa: F811
+    """131072 keys.  A weight times a value scale is rounded to fp16, by 2^-11 at the most and independently of the
+    others: a root mean square of 2^-11 / sqrt(3) of each term, and as much of the output, whose terms have either
+    sign alike.  Six of those deviations cover the 4096 outputs; the scores' and sums' fp32 errors are far below."""
+    L = 131072
+    cache = Q.random_cache(93, 1, L, hkv, d)
+    q = Q.normal(94, 1, hq, d)
+    cos, sin = Q.tables(L, d)
+    out, lse = jl.jl_bifocal_decode_q4(q, *cache, Q.dev([L], torch.int32), L, w0, w_pre, cos, sin)
+    jl.jl_sync_status()
+    want, want_lse = expect_gpu(q[0], [x[0] for x in cache], L, w0, w_pre)
+    assert excess(out[0], want) <= 6 * 2.0**-11 / 3**0.5
+    assert (lse[0] - want_lse).abs().max().item() <= 2e-5
