@@ -468,6 +468,9 @@ jl_status jl_kv_cache_read_q4_paged(const void* k_codes, const void* v_codes, co
  *   workspace    at least jl_bifocal_decode_q4_workspace_size(Hq, head_dim) bytes, 16-byte
  *                aligned, whatever the batch and the lengths; its contents on entry do not
  *                matter; calls that share it must not overlap
+ * Value scales may be of any size and differ between the groups of a row.  Between keys, what
+ * counts is weight * scale of a head and group: a key's values keep 11 bits down to 2^-20 of the
+ * largest, and drop out below 2^-31 of it.
  * Cache rows behind an entry's length may hold anything, NaN scales too.  Paged: page_size
  * is a multiple of 16; a page outside [0, num_pages) is read as zeros and reported by
  * jl_sync_status() as JL_ERR_INVALID.  Supported: head_dim 64 or 128, 1 to 16 query heads

@@ -160,11 +160,13 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 // Weights are multiplied by the value scales of their key in fp32 and rounded to fp16 (2^-11 of
 // each), three bits more than the bf16 of the cached values' scales and of the output: the output
 // is off by 2.0e-4 of its size from it at every length, beside 1.67e-3 of its own rounding.  A second
-// fp16 number for the rest would double the values' matrix instructions.  So that the products fit fp16 whatever the scales, the softmax's reference M is
-// not the largest score but follows the largest score + log2(largest scale of the key): M
-// keeps weight * scale = 2^(score - M) * scale at or below 2^14, where it was 2^10 when M last
-// moved, and products down to 2^-34 of the largest still count.  Numerator and denominator
-// share M, so it drops out.  Sums and outputs are held in fp32.
+// fp16 number for the rest would double the values' matrix instructions.  So that the products fit
+// fp16 whatever the scales, each head and value group has a factor of its own, a power of two
+// that keeps weight * scale * factor at or below 2^15, where it was 2^7 when it last moved:
+// products down to 2^-20 of the group's largest keep 11 bits, and down to 2^-31 still count.
+// The softmax's reference M is the largest score when it last moved and moves before a weight
+// passes 2^8; a key that has all the weight has a weight of 1 and gives its values exactly.  The factors are taken off the sums at the end.  Sums and outputs
+// are held in fp32.
 //
 // The rotations' cos and sin are the same for all heads, so three warps make them once a tile
 // for the whole head block: from the table's row of a run's first key by steps of one position
@@ -632,12 +634,17 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
       key_warps_sync();
 
       float o[NP][MT][4], m[NQ], l[NQ], mul[NQ];
+      // Factors of the value groups (two fp32 each), powers of two from 2^-119 to 2^119, and the
+      // largest of this lane's heads.
+      uint64_t fac[NQ][2], fac_max[2] = {f2_pack(0x1p119f, 0x1p119f), f2_pack(0x1p119f, 0x1p119f)};
       uint4 qf[kQueryRegs ? NQ * KW : 1];
       int have = -1;  // the variant that qf holds
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         m[n] = -INFINITY;
         l[n] = 0.f;
+#pragma unroll
+        for (int f = 0; f < 2; ++f) fac[n][f] = f2_pack(0x1p119f, 0x1p119f);
         mul[n] = sh.mul[head * 4 * NQ + 4 * n + t];
       }
 #pragma unroll
@@ -741,11 +748,16 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
         }
       };
 
-      // Weights of sixteen keys and their products with the value scales.  M moves only when a
-      // product passes 2^14 (in the first keys: by anything), so it rarely does.
+      // Weights of sixteen keys and their products with the value scales.  M and the factors move
+      // when a weight passes 2^8 or a product 2^15 (in the first keys: by anything), then those of
+      // all heads, each with eight octaves to spare: with only the ones that had to, or four
+      // octaves, they moved so often that groups of five and more heads took 10 to 20 % longer.
       auto weights = [&](int u, float (&s)[NQ][2], auto tail_tag) {
         constexpr bool TAIL = decltype(tail_tag)::value;
         uint2 vs[2];
+        uint64_t vf[2][2];  // two fp32 each
+        float wt[NQ][2];
+        bool over = false;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           vs[r] = lds64(base + at_scale + u * next_scales + r * 128 * HPB + 8);
@@ -754,61 +766,93 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
 #pragma unroll
             for (int n = 0; n < NQ; ++n) s[n][r] = -INFINITY;
           }
-        }
-        float wt[NQ][2], vf[2][4];
-        bool over = false;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          vf[r][0] = bf16_low(vs[r].x), vf[r][1] = bf16_high(vs[r].x), vf[r][2] = bf16_low(vs[r].y), vf[r][3] = bf16_high(vs[r].y);
-          const float top = fmaxf(fmax3(vf[r][0], vf[r][1], vf[r][2]), fmaxf(vf[r][3], 0x1p-90f));
+          vf[r][0] = f2_pack(bf16_low(vs[r].x), bf16_high(vs[r].x));
+          vf[r][1] = f2_pack(bf16_low(vs[r].y), bf16_high(vs[r].y));
+          // what a weight is multiplied by at the most, known before the scores are
+          float x[4];
+          f2_unpack(f2_mul(vf[r][0], fac_max[0]), x[0], x[1]);
+          f2_unpack(f2_mul(vf[r][1], fac_max[1]), x[2], x[3]);
+          const float top = fmax3(fmax3(x[0], x[1], x[2]), x[3], 0x1p7f);
 #pragma unroll
           for (int n = 0; n < NQ; ++n) {
-            wt[n][r] = ex2_approx(fmaf(s[n][r], mul[n], -m[n]));
-            over |= wt[n][r] * top > 0x1p14f;
+            wt[n][r] = ex2_approx(__fmul_rn(s[n][r], mul[n]) - m[n]);  // 1 where the score is M
+            over |= wt[n][r] * top > 0x1p15f;
           }
         }
         if (__any_sync(0xffffffffu, over)) {
-          float f[NQ];
+          float by[NQ][4], most[4] = {};
 #pragma unroll
           for (int n = 0; n < NQ; ++n) {
-            float top = m[n] + 10.f;
+            float top[5];  // of the scores and the groups' scales, and of the scores
+            top[4] = fmaxf(__fmul_rn(s[n][0], mul[n]), __fmul_rn(s[n][1], mul[n]));
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float big = fmaxf(fmax3(vf[r][0], vf[r][1], vf[r][2]), fmaxf(vf[r][3], 0x1p-90f));
-              top = fmaxf(top, fmaf(s[n][r], mul[n], __log2f(big)));
+            for (int f = 0; f < 4; ++f) {
+              float v[2], w[2];
+              f2_unpack(vf[0][f / 2], v[0], v[1]);
+              f2_unpack(vf[1][f / 2], w[0], w[1]);
+              top[f] = fmaxf(fmaf(s[n][0], mul[n], __log2f(v[f & 1])), fmaf(s[n][1], mul[n], __log2f(w[f & 1])));
             }
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            const float now = top - 10.f;
-            f[n] = m[n] == -INFINITY ? 0.f : ex2_approx(m[n] - now);
-            m[n] = now;
-            l[n] *= f[n];
+            for (int x = 4; x < 32; x <<= 1)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) wt[n][r] = ex2_approx(fmaf(s[n][r], mul[n], -now));
+              for (int f = 0; f < 5; ++f) top[f] = fmaxf(top[f], __shfl_xor_sync(0xffffffffu, top[f], x));
+            const float now = fmaxf(m[n], top[4]);
+            const bool first = m[n] == -INFINITY;
+            l[n] *= first ? 0.f : ex2_approx(m[n] - now);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float fc[2];
+              f2_unpack(fac[n][h], fc[0], fc[1]);
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const int f = 2 * h + z;
+                // log2 of the weight * scale, before M, whose product is 1: as it was, and from now on
+                const float was = first ? -INFINITY : m[n] - (static_cast<int>(__float_as_uint(fc[z]) >> 23) - 127);
+                const float to = fmaxf(was, top[f] - 7.f);
+                const float up = floorf(fminf(119.f, fmaxf(-119.f, now - to)));
+                by[n][f] = first ? 0.f : ex2_approx(was - now + up);  // at most 1
+                fc[z] = __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(up)) << 23);
+                most[f] = fmaxf(most[f], fc[z]);
+              }
+              fac[n][h] = f2_pack(fc[0], fc[1]);
+            }
+            m[n] = now;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) wt[n][r] = ex2_approx(__fmul_rn(s[n][r], mul[n]) - now);
           }
+          fac_max[0] = f2_pack(most[0], most[1]);
+          fac_max[1] = f2_pack(most[2], most[3]);
 #pragma unroll
           for (int n = 0; n < NP; ++n)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float by = f[NQ == 1 ? 0 : 2 * n + (y & 1)];
+            for (int x = 0; x < MT; ++x)
 #pragma unroll
-              for (int x = 0; x < MT; ++x) o[n][x][y] *= by;
-            }
+              for (int y = 0; y < 4; ++y) {
+                const int z = y & 1, f = x * 4 / MT;
+                if constexpr (NQ == 1) o[n][x][y] *= by[0][(f & 2) + z];
+                else o[n][x][y] *= by[2 * n + z][f];
+              }
         }
         // Column 2t of the weights is head t of score tile 2n, column 2t + 1 of tile 2n + 1; with
         // one score tile both are head t, the even columns under the scales of the even groups
         // and the odd ones under those of the odd groups.
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
+          float x[NQ][4];
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) l[n] += wt[n][r];
+          for (int n = 0; n < NQ; ++n) {
+            l[n] += wt[n][r];
+            const uint64_t w2 = f2_pack(wt[n][r], wt[n][r]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)  // the factor first: 2^8 * 2^119 at the most, so that is finite
+              f2_unpack(f2_mul(f2_mul(w2, fac[n][h]), vf[r][h]), x[n][2 * h], x[n][2 * h + 1]);
+          }
 #pragma unroll
           for (int n = 0; n < NP; ++n)
 #pragma unroll
             for (int f = 0; f < kF; ++f) {
-              const float a = wt[NQ == 1 ? 0 : 2 * n][r] * vf[r][NQ == 1 ? 2 * f : f];
-              const float bb = wt[NQ == 1 ? 0 : 2 * n + 1][r] * vf[r][NQ == 1 ? 2 * f + 1 : f];
-              pf[n][f][r] = transpose_8x8(h2_bits(__floats2half2_rn(a, bb)));
+              if constexpr (NQ == 1) pf[n][f][r] = transpose_8x8(h2_bits(__floats2half2_rn(x[0][2 * f], x[0][2 * f + 1])));
+              else pf[n][f][r] = transpose_8x8(h2_bits(__floats2half2_rn(x[2 * n][f], x[2 * n + 1][f])));
             }
         }
       };
@@ -890,6 +934,15 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
       }
 
       // Join the warps that share a head, and write the result or the partial.
+      float unit[NQ][4];  // of the groups' sums
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          f2_unpack(fac[n][h], unit[n][2 * h], unit[n][2 * h + 1]);
+          unit[n][2 * h] = 1.f / unit[n][2 * h];
+          unit[n][2 * h + 1] = 1.f / unit[n][2 * h + 1];
+        }
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -908,8 +961,8 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
           const float inv = 1.f / l[n];
 #pragma unroll
           for (int x = 0; x < MT; ++x) {
-            const int y = NQ == 1 ? (x * 4 / MT) & 1 : n & 1;
-            const float lo = o[n / 2][x][y], hi = o[n / 2][x][2 + y] * 0.0625f;
+            const int f = x * 4 / MT, y = NQ == 1 ? f & 1 : n & 1;
+            const float lo = o[n / 2][x][y] * unit[n][f], hi = o[n / 2][x][2 + y] * (0.0625f * unit[n][f]);
             if (whole) {
               p.out[at * D + 16 * x + g] = __float2bfloat16_rn(lo * inv);
               p.out[at * D + 16 * x + 8 + g] = __float2bfloat16_rn(hi * inv);
@@ -934,9 +987,9 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
         float* row = join + (warp * 4 * NQ + 4 * n + t) * (D + 8) + g;
 #pragma unroll
         for (int x = 0; x < MT; ++x) {
-          const int y = NQ == 1 ? (x * 4 / MT) & 1 : n & 1;  // the column that holds this head under this group's scales
-          row[16 * x] = o[n / 2][x][y];
-          row[16 * x + 8] = o[n / 2][x][2 + y] * 0.0625f;
+          const int f = x * 4 / MT, y = NQ == 1 ? f & 1 : n & 1;  // the column that holds this head under this group's scales
+          row[16 * x] = o[n / 2][x][y] * unit[n][f];
+          row[16 * x + 8] = o[n / 2][x][2 + y] * (0.0625f * unit[n][f]);
         }
       }
       key_warps_sync();

@@ -16,7 +16,7 @@ def uniform_codes(g, *shape):
 
 
 def value_rows(v_codes, scales):
-    """The fp32 values of rows [..][d/2], [..][8], on the GPU."""
+    """The fp32 values of rows [..][d/2], [..][8], on the GPU (exact: four bits times eight)."""
     d = 2 * v_codes.shape[-1]
     place = [Q.R.value_place(d, c) for c in range(d)]
     byte = torch.tensor([b for b, _ in place], device="cuda")
@@ -43,7 +43,9 @@ def rope64(x, pos):
 
 
 def expect_gpu(q, cache, L, w0, w_pre):
-    """The definition in 64 bits on the GPU: q [hq][d], cache rows [stride][hkv][..] of one entry -> out, lse."""
+    """The definition in 64 bits on the GPU: q [hq][d], cache rows [stride][hkv][..] of one entry -> out, lse, and
+    what errors are relative to: the sums of the weights times the values' sizes, and by channel the largest weight
+    times value scale."""
     k, v = key_rows(cache[0][:L], cache[2][:L]).double(), value_rows(cache[1][:L], cache[2][:L]).double()
     grow, i = max(1, -(-L // w_pre)), L - 1
     edge = max(0, min(L, i - w0 + 1)) if grow > 1 else 0  # keys before it are remote
@@ -54,7 +56,10 @@ def expect_gpu(q, cache, L, w0, w_pre):
     kv = torch.arange(q.shape[0], device="cuda") // (q.shape[0] // k.shape[1])
     k, v = k.transpose(0, 1)[kv], v.transpose(0, 1)[kv]  # [hq][L][d]
     s = torch.cat([(k[:, :edge] @ far[:, :, None]), (k[:, edge:] @ near[:, :, None])], 1)[..., 0] / q.shape[1] ** 0.5
-    return (torch.softmax(s, -1)[:, None] @ v)[:, 0], torch.logsumexp(s, -1)
+    w = torch.softmax(s, -1)
+    step = cache[2][:L].double()[..., 4:].transpose(0, 1)[kv]  # [hq][L][4]
+    most = (w[..., None] * step).amax(1).repeat_interleave(q.shape[1] // 4, 1)
+    return (w[:, None] @ v)[:, 0], torch.logsumexp(s, -1), (w[:, None] @ v.abs())[:, 0], most
 
 
 def excess(out, want):
@@ -128,7 +133,7 @@ def test_many_keys_a_warp_relative_to_their_size(jl, B, L, hq, hkv, d):  # noqa:
     out, lse = jl.jl_bifocal_decode_q4(q, kc, vc, sc, Q.dev([L] * B, torch.int32), L, 0, L, tab, tab)
     jl.jl_sync_status()
     for b in (0, B // 2, B - 1):
-        want, want_lse = expect_gpu(q[b], (kc[b], vc[b], sc[b]), L, 0, L)
+        want, want_lse, _, _ = expect_gpu(q[b], (kc[b], vc[b], sc[b]), L, 0, L)
         assert excess(out[b], want) <= 6 * 2.0**-11 / 3**0.5 + 2.0**-13
         assert (lse[b] - want_lse).abs().max().item() <= 2e-5
 
@@ -145,6 +150,62 @@ def test_long_outputs_relative_to_their_size(jl, d, hq, hkv, w0, w_pre):  # noqa
     cos, sin = Q.tables(L, d)
     out, lse = jl.jl_bifocal_decode_q4(q, *cache, Q.dev([L], torch.int32), L, w0, w_pre, cos, sin)
     jl.jl_sync_status()
-    want, want_lse = expect_gpu(q[0], [x[0] for x in cache], L, w0, w_pre)
+    want, want_lse, _, _ = expect_gpu(q[0], [x[0] for x in cache], L, w0, w_pre)
     assert excess(out[0], want) <= 6 * 2.0**-11 / 3**0.5
     assert (lse[0] - want_lse).abs().max().item() <= 2e-5
+
+
+def scale_pattern(name, B, L, hkv):
+    """Factors [B][L][hkv][4] of the value scales."""
+    g = np.random.default_rng(97)
+    groups = np.broadcast_to(np.array([1.0, 1e10, 1e-20, 1e30]), (B, L, hkv, 4))
+    ramp = 10.0 ** np.linspace(-15, 15, L)[None, :, None, None]
+    return {
+        "groups": groups,
+        "bits": np.broadcast_to(2.0 ** np.array([-97, 0, 50, 110]), (B, L, hkv, 4)),
+        "keys": 10.0 ** g.uniform(-20, 20, (B, L, hkv, 1)) * np.ones(4),
+        "both": 10.0 ** g.uniform(-20, 20, (B, L, hkv, 4)),
+        "growing": ramp * np.ones((B, L, hkv, 4)),
+        "falling": 1 / ramp * np.array([1.0, 1e10, 1e-20, 1e20]),
+        "zeros first": np.where(np.arange(L)[None, :, None, None] < 500, 0.0, groups),
+        "zeros last": np.where(np.arange(L)[None, :, None, None] < 40, groups, 0.0),
+        "one group of zeros": groups * np.array([1.0, 0.0, 1.0, 1.0]),
+    }[name]
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(128, 32, 8), (128, 3, 3), (64, 8, 2), (128, 12, 2), (64, 6, 1), (128, 16, 1), (64, 9, 1)])
+@pytest.mark.parametrize("pattern", ["groups", "bits", "keys", "both", "growing", "falling", "zeros first", "zeros last",
+                                     "one group of zeros"])
+def test_value_scales_of_any_size(jl, d, hq, hkv, pattern):  # noqa: F811
+    """Each channel against what its own weights and values allow.  A weight times a scale is rounded to fp16, by 2^-11
+    of it or, among subnormals, by 2^-25, where the largest of its group was 2^6 at least when the factor was set:
+    2^-31 of that for each key, times a code of 7.  The scores are off by some 2e-5 (2^-15) and the fp32 sums by less;
+    the output by half a bf16 step."""
+    lens = (777, 30)
+    cache = list(Q.random_cache(98, 2, 777, hkv, d))
+    factor = torch.from_numpy(scale_pattern(pattern, 2, 777, hkv).copy()).cuda()
+    cache[2][..., 4:] = (cache[2][..., 4:].double() * factor).bfloat16()
+    q = Q.normal(99, 2, hq, d)
+    cos, sin = Q.tables(777, d)
+    out, lse = jl.jl_bifocal_decode_q4(q, *cache, Q.dev(lens, torch.int32), 777, 50, 300, cos, sin)
+    jl.jl_sync_status()
+    for b, L in enumerate(lens):
+        rows = [x[b] for x in cache]
+        want, want_lse, size, most = expect_gpu(q[b], rows, L, 50, 300)
+        step = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=2.0**-126))) - 8)
+        assert bool(((out[b].double() - want).abs() <= step + (2.0**-11 + 2.0**-15) * size + 7 * L * 2.0**-31 * most).all())
+        assert (lse[b] - want_lse).abs().max().item() <= 2e-5
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(128, 32, 8), (64, 8, 2), (128, 12, 2), (128, 16, 1)])
+def test_a_lone_key_gives_its_values(jl, d, hq, hkv):  # noqa: F811
+    """Lengths of one: the weight is 1, so a product with a bf16 scale is exact in fp16, and the output
+    is the key's value rounded once, ties included."""
+    B = 9
+    cache = Q.random_cache(95, B, 4, hkv, d)
+    q = Q.normal(96, B, hq, d)
+    cos, sin = Q.tables(4, d)
+    out, _ = jl.jl_bifocal_decode_q4(q, *cache, Q.dev([1] * B, torch.int32), 4, 2, 3, cos, sin)
+    jl.jl_sync_status()
+    want = value_rows(cache[1][:, 0], cache[2][:, 0]).bfloat16().repeat_interleave(hq // hkv, 1)
+    assert torch.equal(out, want)
