@@ -401,6 +401,11 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
               if (!there) atomicOr(&g_status, kDevErrBounds);
               row = (there ? page : p.num_pages) * p.page_size + (there ? j % p.page_size : 0);  // outside reads zeros
             }
+            JL_CHECK(j >= L || p.block_table != nullptr ||
+                     (j < p.cache_stride && row >= 0 && row < static_cast<int64_t>(p.B) * p.cache_stride));
+            JL_CHECK(j >= L || p.block_table == nullptr || (j < p.max_pages * static_cast<int64_t>(p.page_size) && row >= 0 &&
+                                                            row <= static_cast<int64_t>(p.num_pages) * p.page_size));
+            JL_CHECK(b >= 0 && b < p.B && (hb + 1) * HPB <= p.Hkv);
           }
           if (!warp_wait(&sh.empty[stage], phase ^ 1, abort)) {
             ok = false;
@@ -574,6 +579,7 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
       {
         constexpr int kRows = 32 / kDecodeQ4KeyWarps;  // HPB * NQ <= 8
         const int nq = i - i / grow;
+        JL_CHECK(nq >= 0 && nq < p.n_tab_rows && b < p.B && (hb + 1) * HPB * p.group <= p.Hq);
         const bool has = D == 128 || lane < 16;
         const int w = D == 128 ? lane / 8 : (lane & 15) / 8, ft = D == 128 ? (lane / 2) & 3 : lane & 3;
         const int e = D == 128 ? lane & 1 : (lane >> 2) & 1;
@@ -951,6 +957,9 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
       const int hpb = HPB * p.group;
       const int slot0 = (cur == st.begin ? 0 : p.n_cta) + blockIdx.x;  // query head q's partial: slot0 + 2 q n_cta
       float* ml = p.ws + static_cast<int64_t>(p.n_cta) * 2 * hpb * D;
+      // two partials a CTA and head of a block, the first or the last segment of its range
+      JL_CHECK(whole || (slot0 + 2 * (hpb - 1) * p.n_cta < 2 * hpb * p.n_cta && hpb <= p.Hq &&
+                         (cur == st.begin || cur + t1 - t0 == st.end)));
       if (wph == 1) {  // this warp has all of its head: straight from its registers
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
@@ -1070,6 +1079,7 @@ __global__ void __launch_bounds__(kCombineQ4Threads) jl_decode_q4_combine_kernel
   auto slot = [&](int c) { return (2 * q + (c == 0 ? s0 : 0)) * p.n_cta + c0 + c; };
   const float* ml = p.ws + static_cast<int64_t>(p.n_cta) * 2 * hpb * D;
   const bool wrong = L < 0 || L > p.max_seqlen;
+  JL_CHECK(count == 0 || (c0 >= 0 && c1 < p.n_cta && count <= 32 * OWN && (2 * q + 1) * p.n_cta + c1 < 2 * hpb * p.n_cta));
   griddep_wait();
   const bool bad = wrong || status_failed();
   float2 own[OWN];  // maxima and sums, lane + 32 x

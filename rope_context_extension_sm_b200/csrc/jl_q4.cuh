@@ -66,6 +66,11 @@ __device__ __forceinline__ int64_t q4_row(const Q4Params& p, int b, int64_t pos)
   return static_cast<int64_t>(page) * p.page_size + (x - n * p.page_size);
 }
 
+// Rows of the cache, contiguous or paged (debug-bounds checks).
+__device__ __forceinline__ int64_t q4_rows(const Q4Params& p) {
+  return p.block_table != nullptr ? static_cast<int64_t>(p.num_pages) * p.page_size : p.batch * p.cache_stride;
+}
+
 // The scale of a group from the largest |x| of it, given as float bits (so that a NaN or an
 // infinity stays the largest).
 __device__ __forceinline__ __nv_bfloat16 q4_scale(uint32_t top_bits) {
@@ -281,6 +286,8 @@ __global__ void __launch_bounds__(4 * kQ4Teams, 3) jl_kv_fill_q4_kernel(const Q4
       live = false;
     }
   }
+  JL_CHECK(!live || (row < p.total_tokens * p.Hkv && pos < p.n_tab_rows && crow >= 0 && crow < q4_rows(p) && h >= 0 &&
+                     h < p.Hkv));
   q4_write_row<D>(p, live, p.k + row * D, p.v + row * D, pos, crow, h, w);
 }
 
@@ -299,6 +306,7 @@ __global__ void __launch_bounds__(4 * kQ4Teams) jl_decode_append_q4_kernel(const
       return;
     }
     const int64_t o = warp * D;
+    JL_CHECK(warp / p.Hq < p.batch && i < p.n_tab_rows);
 #pragma unroll
     for (int e = 0; e < PPL; ++e) {
       const int c = lane * PPL + e;
@@ -323,6 +331,8 @@ __global__ void __launch_bounds__(4 * kQ4Teams) jl_decode_append_q4_kernel(const
       live = false;
     }
   }
+  JL_CHECK(!live || (row < static_cast<int64_t>(p.batch) * p.Hkv && i < p.n_tab_rows && crow >= 0 && crow < q4_rows(p) &&
+                     h >= 0 && h < p.Hkv));
   q4_write_row<D>(p, live, p.k + row * D, p.v + row * D, i, crow, h, w);
 }
 
@@ -372,6 +382,8 @@ __global__ void __launch_bounds__(4 * kQ4Teams) jl_kv_read_q4_kernel(const Q4Par
     }
     r = crow * p.Hkv + h;
   }
+  JL_CHECK(!live || (r >= 0 && r < q4_rows(p) * p.Hkv && row < static_cast<int64_t>(p.batch) * p.out_rows * p.Hkv &&
+                     in_entry < p.out_rows * p.Hkv && pos < p.cache_stride));
   uint4 kw = make_uint4(0u, 0u, 0u, 0u), vw = kw;  // this lane's quarter of the codes
   uint32_t ks = 0, vs = 0;
   if (live) {
