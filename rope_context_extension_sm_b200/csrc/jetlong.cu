@@ -611,11 +611,13 @@ jl_status q4_common(Q4Op op, jl::Q4Params& prm, int64_t rows, int32_t head_dim, 
   for (const void* x : all)
     if (!aligned16(x)) return fail(JL_ERR_INVALID, "every tensor must be 16-byte aligned");
   // rows of (token, head), four lanes each; an append's queries take a warp each before them
-  const int64_t tokens = op != Q4Op::kRead ? rows : rows > 0x7fffffffLL ? rows : prm.batch * rows;
-  const int64_t n = tokens > 0x7fffffffLL ? 0 : tokens * prm.Hkv;
-  const int64_t lanes = op == Q4Op::kAppend ? 32 * (tokens * prm.Hq + (n + 7) / 8) : 4 * n;
-  if (tokens > 0x7fffffffLL || lanes > 0x7fffffffLL * 256 || (op == Q4Op::kRead && prm.batch > 65535))
+  constexpr int64_t kMost = 0x7fffffffLL;
+  const int64_t tokens = op != Q4Op::kRead ? rows : rows > kMost ? rows : prm.batch * rows;
+  const int64_t a_token = op == Q4Op::kAppend ? 32LL * prm.Hq + 4LL * prm.Hkv : 4LL * prm.Hkv;  // lanes
+  if (tokens > kMost || tokens > (kMost * 256 - 32) / a_token || (op == Q4Op::kRead && prm.batch > 65535))
     return fail(JL_ERR_UNSUPPORTED, "too many rows for one call (%lld)", (long long)tokens);
+  const int64_t n = tokens * prm.Hkv;
+  const int64_t lanes = op == Q4Op::kAppend ? 32 * (tokens * prm.Hq + (n + 7) / 8) : 4 * n;
   const unsigned blocks = static_cast<unsigned>((lanes + 255) / 256);
   const bool wide = head_dim == 128;
   if (op == Q4Op::kFill) {
@@ -751,10 +753,12 @@ jl_status dispatch_decode_q4(jl::DecodeQ4Params& prm, cudaStream_t st) {
   // Score tiles of four query heads (two columns each in an n = 8 matrix instruction); KV heads
   // of a block, which share its cos/sin rows, as many as eight key warps and 32 KB of query
   // fragments allow; sixteens of keys of a warp in a tile, as many as leave two stages of shared
-  // memory.  More hide more latency: at 128K keys of 128 channels (measured with half the cos/sin
-  // rows) 45.9 us with four against 50.5 with two for 32/8 heads, 36.8 with two against 40.6 with
-  // one for 32/4; one stage alone costs more than that (24/3 heads: 46.7 us with two sixteens in
-  // one stage, 39.1 with one in two).  Eight query heads leave registers for two, sixteen for one.
+  // memory.  More hide more latency, one stage alone costs more than that: at 128K keys of 128
+  // channels and 32/8 heads 64.0 us with two sixteens, 74.1 with one, 75.4 with four in one stage;
+  // 64/8 80.3 with two, 89.0 with one; 24/3 60.5 with one, 65.9 with two in one stage.  Eight query
+  // heads leave registers for two, sixteen for one.  Nine to sixteen query heads of 128 channels on
+  // an odd number of KV heads have one stage all the same: half of the memory is the join's, and
+  // one sixteen is the least.
   const int nq = prm.group <= 4 ? 1 : prm.group <= 8 ? 2 : 4;
   int hpb = 8 / nq;
   while (prm.Hkv % hpb != 0) hpb /= 2;
@@ -806,8 +810,8 @@ jl_status decode_q4(jl::DecodeQ4Params prm, int32_t head_dim, float softmax_scal
   if (prm.n_tab_rows < prm.max_seqlen)
     return fail(JL_ERR_INVALID, "n_tab_rows (%lld) must be >= max_seqlen (%d)", (long long)prm.n_tab_rows,
                 prm.max_seqlen);
-  if (!paged && prm.B * prm.cache_stride > 0x7fffffffLL)
-    return fail(JL_ERR_UNSUPPORTED, "B * cache_stride must be < 2^31 (got %lld)", (long long)(prm.B * prm.cache_stride));
+  if (!paged && prm.cache_stride > 0x7fffffffLL / prm.B)
+    return fail(JL_ERR_UNSUPPORTED, "B * cache_stride must be < 2^31 (got %d * %lld)", prm.B, (long long)prm.cache_stride);
   if (prm.B > 65535 || prm.Hkv > 65535)  // dimensions of the combine's grid
     return fail(JL_ERR_UNSUPPORTED, "B and Hkv must be <= 65535 (got %d, %d)", prm.B, prm.Hkv);
   if (!prm.q || !prm.k_codes || !prm.v_codes || !prm.scales || !prm.seqlens || !prm.cos_tab || !prm.sin_tab ||
