@@ -739,10 +739,16 @@ jl_status launch_decode_q4(const jl::DecodeQ4Params& prm, cudaStream_t st) {
                 attr.regs, jl::kDecodeQ4Regs);
   cudaError_t e = launch_pdl(kern, dim3(prm.n_cta), dim3(jl::kDecodeQ4Threads), smem, st, tk, tv, ts, prm);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit decode launch");
-  // Four blocks a head while that leaves room on the SMs (148 of four or more blocks each).
+  // Four blocks a head while that leaves room on the SMs (148 of four or more blocks each).  By
+  // ranges from where there are half as many entries and head blocks again (fewer blocks, and a scan
+  // of the lengths for each range instead of each entry and warp): 32/8 heads of 128, 150 entries
+  // of 512 keys 50.0 us by ranges, 46.8 by entries; 256 of 512 68.2 and 71.7; 4096 of 32 291 and 2386.
   const bool split = static_cast<int64_t>(prm.Hq) * prm.B * 4 <= 1024;
-  e = launch_pdl(split ? jl::jl_decode_q4_combine_kernel<D, 4> : jl::jl_decode_q4_combine_kernel<D, 1>,
-                 dim3(prm.heads_per_block * prm.group * (split ? 4 : 1), prm.B, prm.Hkv / prm.heads_per_block),
+  const int head_blocks = prm.Hkv / prm.heads_per_block, heads = prm.heads_per_block * prm.group;
+  const bool ranges = static_cast<int64_t>(prm.B) * head_blocks * 2 > prm.n_cta * 3;
+  const auto combine = split ? (ranges ? jl::jl_decode_q4_combine_kernel<D, 4, true> : jl::jl_decode_q4_combine_kernel<D, 4, false>)
+                             : (ranges ? jl::jl_decode_q4_combine_kernel<D, 1, true> : jl::jl_decode_q4_combine_kernel<D, 1, false>);
+  e = launch_pdl(combine, dim3(heads * (split ? 4 : 1), ranges ? prm.n_cta : prm.B, ranges ? 1 : head_blocks),
                  dim3(jl::kCombineQ4Threads), 0, st, prm);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit decode combine launch");
   return ok();

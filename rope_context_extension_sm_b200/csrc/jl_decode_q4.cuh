@@ -84,17 +84,11 @@ struct Q4Start {
   int begin, end;  // the range in the list of all tiles (the host keeps their number below 2^31)
 };
 
-__device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
-  Q4Start s{};
-  int t;
-  const int all = q4_tiles_before(p, 0, lane, t).x;
-  const int total = all * (p.Hkv / p.heads_per_block);
-  const int per = q4_per_cta(p, total);
-  s.begin = min(static_cast<int64_t>(total), static_cast<int64_t>(per) * blockIdx.x);
-  s.end = s.begin + min(per, total - s.begin);
-  if (s.begin >= s.end) return s;
-  s.hb = s.begin / all;
-  int left = s.begin % all;
+// The place of tile `at` of the list, by one warp; `all`: the tiles of a head block, `t`: those of
+// entry `lane`.
+__device__ __forceinline__ void q4_place(const DecodeQ4Params& p, int lane, int at, int all, int t, Q4Start& s) {
+  s.hb = at / all;
+  int left = at % all;
   for (int e0 = 0; e0 < p.B; e0 += 32) {
     const int e = e0 + lane, len = e < p.B ? p.seqlens[e] : 0;
     if (e0 > 0) t = q4_tiles(p, len);
@@ -110,10 +104,21 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
       s.b = e0 + src;
       s.tile = left - __shfl_sync(0xffffffffu, sum - t, src);
       s.len = __shfl_sync(0xffffffffu, len, src);
-      return s;
+      return;
     }
     left -= __shfl_sync(0xffffffffu, sum, 31);
   }
+}
+
+__device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
+  Q4Start s{};
+  int t;
+  const int all = q4_tiles_before(p, 0, lane, t).x;
+  const int total = all * (p.Hkv / p.heads_per_block);
+  const int per = q4_per_cta(p, total);
+  s.begin = min(static_cast<int64_t>(total), static_cast<int64_t>(per) * blockIdx.x);
+  s.end = s.begin + min(per, total - s.begin);
+  if (s.begin < s.end) q4_place(p, lane, s.begin, all, t, s);
   return s;
 }
 
@@ -1055,33 +1060,87 @@ constexpr int kCombineQ4Threads = 256;
 // against 0.9).  Every warp asks at once for the maxima and sums of all partials, which it
 // needs for its weights, and for its channels of the first ones: one round trip and one
 // barrier for up to 148 partials.
-template <int D, int SPLIT>
+//
+// RANGES false: blockIdx.y is an entry, blockIdx.z its head block; every warp adds up the tiles of
+// the entries before it.  Of a large batch that is quadratic, and only the entries that two ranges
+// share, one for each CTA at the most, have something to join.  RANGES true: blockIdx.y is the
+// CTA in whose range such an entry begins, found by one warp; the entries that have no keys are
+// shared out over the same blocks.
+template <int D, int SPLIT, bool RANGES>
 __global__ void __launch_bounds__(kCombineQ4Threads) jl_decode_q4_combine_kernel(const DecodeQ4Params p) {
   constexpr int NW = kCombineQ4Threads / 32, CH = D / SPLIT, LANES = CH / 4;  // a float4 a lane
   constexpr int ROWS = kCombineQ4Threads / LANES, PER = 5;                    // partials at a time, and rounds in flight
   constexpr int OWN = (kDecodeQ4Ctas + 31) / 32;
   __shared__ float weight[NW][32 * OWN];
   __shared__ __align__(16) float sum[NW][CH];
-  const int hpb = p.heads_per_block * p.group, hb = blockIdx.z, q = blockIdx.x / SPLIT;  // head block, head in it
+  const int hpb = p.heads_per_block * p.group, q = blockIdx.x / SPLIT;  // head of its block
   const int ch = blockIdx.x % SPLIT * CH + threadIdx.x % LANES * 4, row = threadIdx.x / LANES;
-  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_launch_dependents();
   // The decode lets this kernel start only after it waited for everything before it, so the
   // lengths are there; its own partials and the status word are there after the wait.
-  const int L = p.seqlens[b], t = q4_tiles(p, L);
-  int unused;
-  const int2 n = q4_tiles_before(p, b, lane, unused);
-  const unsigned per = max(1, q4_per_cta(p, n.x * (p.Hkv / p.heads_per_block))), first = hb * n.x + n.y;
-  const int c0 = first / per, c1 = t ? (first + t - 1) / per : c0;
-  const int s0 = c0 * per == first ? 0 : 1;
-  const int count = c1 > c0 ? c1 - c0 + 1 : 0;  // 0: the decode wrote the result, or there is none
+  int b, hb, c0, s0, count;  // the entry and its head block, its first CTA and that one's slot, its CTAs
+  bool wrong = false, none = false;
+  if constexpr (!RANGES) {
+    b = blockIdx.y;
+    hb = blockIdx.z;
+    const int L = p.seqlens[b], t = q4_tiles(p, L);
+    int unused;
+    const int2 n = q4_tiles_before(p, b, lane, unused);
+    const unsigned per = max(1, q4_per_cta(p, n.x * (p.Hkv / p.heads_per_block))), first = hb * n.x + n.y;
+    c0 = first / per;
+    const int c1 = t ? (first + t - 1) / per : c0;
+    s0 = c0 * per == first ? 0 : 1;
+    count = c1 > c0 ? c1 - c0 + 1 : 0;  // 0: the decode wrote the result, or there is none
+    wrong = L < 0 || L > p.max_seqlen;
+    none = t == 0;
+  } else {
+    __shared__ int found[5];
+    if (warp == 0) {
+      Q4Start s{};
+      int t, joined = 0, slot0 = 0;
+      const int all = q4_tiles_before(p, 0, lane, t).x, total = all * (p.Hkv / p.heads_per_block);
+      const int64_t per = q4_per_cta(p, total), begin = per * blockIdx.y, next = begin + per;
+      if (next < total) {
+        q4_place(p, lane, static_cast<int>(next), all, t, s);
+        const int64_t first = next - s.tile;  // of the entry that has the next range's first tile
+        if (s.tile > 0 && first >= begin) {
+          joined = static_cast<int>((first + q4_tiles(p, s.len) - 1) / per) - static_cast<int>(blockIdx.y) + 1;
+          slot0 = first == begin ? 0 : 1;
+        }
+      }
+      if (lane == 0) found[0] = s.b, found[1] = s.hb, found[2] = blockIdx.y, found[3] = slot0, found[4] = joined;
+    }
+    __syncthreads();
+    b = found[0], hb = found[1], c0 = found[2], s0 = found[3], count = found[4];
+  }
   // the partials of a head lie side by side: by CTA, first those of segments that begin a range
   auto slot = [&](int c) { return (2 * q + (c == 0 ? s0 : 0)) * p.n_cta + c0 + c; };
   const float* ml = p.ws + static_cast<int64_t>(p.n_cta) * 2 * hpb * D;
-  const bool wrong = L < 0 || L > p.max_seqlen;
-  JL_CHECK(count == 0 || (c0 >= 0 && c1 < p.n_cta && count <= 32 * OWN && (2 * q + 1) * p.n_cta + c1 < 2 * hpb * p.n_cta));
+  JL_CHECK(count == 0 || (c0 >= 0 && c0 + count <= p.n_cta && count <= 32 * OWN && b < p.B && (hb + 1) * hpb <= p.Hq));
+  JL_CHECK(count == 0 || slot(count - 1) < 2 * hpb * p.n_cta);
+  // zeros and -inf, or NaN, for head q of head block `of` of entry e
+  auto write_none = [&](int e, int of, bool nan, bool report) {
+    const float x = nan ? __int_as_float(0x7fc00000) : 0.f;
+    const int64_t to = static_cast<int64_t>(e) * p.Hq + of * hpb + q;
+    if (row == 0) *reinterpret_cast<uint2*>(p.out + to * D + ch) = make_uint2(pack_bf16x2(x, x), pack_bf16x2(x, x));
+    if (threadIdx.x == 0 && blockIdx.x % SPLIT == 0) {
+      if (p.lse != nullptr) p.lse[to] = nan ? x : -INFINITY;
+      if (report && q == 0) atomicOr(&g_status, kDevErrBounds);
+    }
+  };
   griddep_wait();
-  const bool bad = wrong || status_failed();
+  bool failed = false;
+  if constexpr (RANGES) {
+    failed = status_failed();
+    for (int e = blockIdx.y; e < p.B; e += gridDim.y) {
+      const int L = p.seqlens[e];
+      const bool outside = L < 0 || L > p.max_seqlen;
+      if (failed || outside || L == 0)
+        for (int of = 0; of < p.Hkv / p.heads_per_block; ++of) write_none(e, of, failed || outside, outside);
+    }
+    if (failed) return;
+  }
   float2 own[OWN];  // maxima and sums, lane + 32 x
 #pragma unroll
   for (int x = 0; x < OWN; ++x)
@@ -1095,14 +1154,12 @@ __global__ void __launch_bounds__(kCombineQ4Threads) jl_decode_q4_combine_kernel
   };
   ask(row);
   const int64_t at = static_cast<int64_t>(b) * p.Hq + hb * hpb + q;
-  if (bad || t == 0) {  // the same for all threads: nothing sets the status word meanwhile but this
-    const float x = bad ? __int_as_float(0x7fc00000) : 0.f;
-    if (row == 0) *reinterpret_cast<uint2*>(p.out + at * D + ch) = make_uint2(pack_bf16x2(x, x), pack_bf16x2(x, x));
-    if (threadIdx.x == 0 && blockIdx.x % SPLIT == 0) {
-      if (p.lse != nullptr) p.lse[at] = bad ? x : -INFINITY;
-      if (wrong && q == 0) atomicOr(&g_status, kDevErrBounds);
+  if constexpr (!RANGES) {
+    failed = status_failed();  // after the loads above are asked for: 0.7 us less
+    if (failed || none) {  // the same for all threads: nothing sets the status word meanwhile but this
+      write_none(b, hb, failed || wrong, wrong);
+      return;
     }
-    return;
   }
   if (count == 0) return;
   float mx = own[0].x;

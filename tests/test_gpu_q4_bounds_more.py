@@ -3,6 +3,7 @@ size, lengths of one to many tiles a CTA, pages of the writers that the decode d
 import pytest
 
 import test_gpu_q4 as Q
+import test_gpu_q4_batches as B
 import test_gpu_q4_sums as S
 import test_gpu_q4_window as W
 from test_gpu_bounds import jlb  # noqa: F401  (the fixture: the binding on libjetlong_bounds.so)
@@ -17,9 +18,14 @@ def test_bounds_build_windows_and_lengths(jlb, d, hq, hkv):  # noqa: F811
     S.test_value_scales_of_any_size(jlb, d, hq, hkv, "both")
 
 
-@pytest.mark.parametrize("B,L", [(1, 4737), (3, 2000), (300, 9)])
-def test_bounds_build_shares_of_the_ctas(jlb, B, L):  # noqa: F811
-    Q.test_batches_and_lengths_share_the_ctas(jlb, B, L)
+@pytest.mark.parametrize("batch,L", [(1, 4737), (3, 2000), (300, 9)])
+def test_bounds_build_shares_of_the_ctas(jlb, batch, L):  # noqa: F811
+    Q.test_batches_and_lengths_share_the_ctas(jlb, batch, L)
+
+
+@pytest.mark.parametrize("name", ["tiny", "odd heads", "head blocks", "one long among many", "long ones"])
+def test_bounds_build_large_batches(jlb, name):  # noqa: F811
+    B.test_large_batches(jlb, name)
 
 
 def test_bounds_build_writers_and_reader(jlb):  # noqa: F811
