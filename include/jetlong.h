@@ -416,7 +416,8 @@ jl_status jl_decode_append_paged(const void* q, const void* k, const void* v, co
  *
  * jl_kv_cache_fill_q4, jl_decode_append_q4: the arguments and the error behaviour of
  * jl_kv_cache_fill and jl_decode_append, with the three tensors for the two caches; a row
- * that is written is written whole, no other row is touched.
+ * that is written is written whole, no other row is touched.  Writers and reader take pages of
+ * any size; a pool that jl_bifocal_decode_q4_paged is to read needs a multiple of 16.
  *
  * jl_kv_cache_read_q4: rows [starts[b], lens[b]) of every entry back to bf16,
  *   k_out[b][p - starts[b]] and v_out[b][p - starts[b]], bf16 [B][out_rows][Hkv][head_dim]

@@ -126,13 +126,15 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 //
 // What bounds it.  A row of 128 channels is 144 bytes: 128K keys of eight heads are 151 MB,
 // 23.0 us at the measured 6.56 TB/s.  Beside that stand, for 16 keys of one head (8192 of
-// those a head at 128K), some 290 warp instructions to expand, weigh and sum 4096 codes and
-// 170 more to rotate the keys, of which the ALU and the fp16 pipe take two cycles each.
-// Measured (graph-replayed, 32/8 heads of 128, cold caches): 61.5 us at 128K keys (G = 4),
-// 2.5 TB/s, of which 52 us are per key and 9 for the start, the first loads and the join;
-// without rotation (G = 1) 28 us are per key.  8K keys take 10.4 us.  With the instructions
-// of the keys and values left out, the loads alone stream 128K keys in 21 us.  So the
-// arithmetic bounds it: issue slots are 48 % used, the FMA pipe 45 %, DRAM 30 %.
+// those a head at 128K), 545 warp instructions in all to expand, weigh and sum 4096 codes and
+// to rotate the keys, of which the ALU and the fp16 pipe take two cycles each.  Measured
+// (graph-replayed, 32/8 heads of 128, cold caches): 63.7 us at 128K keys (G = 4), 2.4 TB/s,
+// of which 54 us are per key and 9 for the start, the first loads and the join; without
+// rotation (G = 1) 30 us are per key.  8K keys take 11.2 us.  With the instructions of the
+// keys and values left out, the loads alone stream 128K keys in 21 us.  So the arithmetic
+// bounds it, although no pipe is full: issue slots are 48 % used, the FMA pipe 44 %, the
+// tensor pipe 17 %, DRAM 27 %.  Two warps a scheduler wait for their own results, for one
+// another's pipes, and (0.5 of a warp at every issue) for instructions to be fetched.
 //
 // Shape.  Eight warps of a CTA take keys; one loads; three make the rotations' factors.  A
 // tile is `tile` keys of all KV heads of a head block: U sixteens of keys of one head for
@@ -157,10 +159,13 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 // and a remainder of at most 2^-8: the codes turned by the first are whole multiples of 2^-7
 // below 2^4, exact in fp16, and turned by the second they are so small that their rounding to
 // 11 bits is some 2^-19 of a code.  Both go through the matrix instruction against the same
-// query, so remote scores are as good as fp32 ones.  With cos, sin and the turned key rounded
-// to fp16 once, scores were off by 3e-4 of a key's part and the lse by 1.4e-6 of itself
-// (5e-8 now, the fp32 sums'); the remainders cost 15 us of the 61.5 at 128K keys.  The group
-// scales are applied to the fp32 sums of their group, between the matrix instructions.
+// query.  A turned channel is off by 7.7e-5 of a code at the most, most of that from the fp32
+// steps of cos and sin below (one key's score of tens: 3e-5 measured, 1/40 of that bound's
+// sum over the channels); over many keys it averages out, and the lse is as good as with fp32
+// scores.  With cos, sin and the turned key rounded to fp16 once, scores were off by 3e-4 of a
+// key's part and the lse by 1.4e-6 of itself (5e-8 now, the fp32 sums'); the remainders cost
+// 15 us of 61.5 at 128K keys when they came.  The group scales are applied to the fp32 sums of
+// their group, between the matrix instructions.
 //
 // Weights are multiplied by the value scales of their key in fp32 and rounded to fp16 (2^-11 of
 // each), three bits more than the bf16 of the cached values' scales and of the output: the output

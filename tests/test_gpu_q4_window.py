@@ -42,6 +42,32 @@ def test_the_windows_edge(jl, d, hq, hkv, w0):  # noqa: F811
         assert bool(((out[b].double() - want).abs() <= step + (2.0**-11 + 1.2e-4) * size).all())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,hq,hkv", [(128, 32, 8), (128, 16, 1), (64, 8, 1), (128, 3, 3)])
+def test_one_remote_key(jl, d, hq, hkv):  # noqa: F811
+    """All keys but one are zero and have the score 0, the one is remote and its score large: the lse shows its error
+    alone.  A turned channel is off by 7.7e-5 of a code at the most (44 steps of cos and sin, 14 * 44 * 2^-24, and the
+    remainders' roundings, 3 * 14 * 2^-8 * 2^-12), so the score by the scale times the sum of the query's channels
+    times that; the fp32 sums by 2^-20 of the score."""
+    B, L, w_pre = 32, 4096, 700
+    g = torch.Generator(device="cuda").manual_seed(8)
+    kc = torch.randint(0, 256, (B, L, hkv, d // 2), generator=g, device="cuda", dtype=torch.uint8)
+    kc = torch.where(kc & 15 == 0, kc | 1, kc)
+    kc = torch.where(kc >> 4 == 0, kc | 16, kc)
+    scales = torch.zeros(B, L, hkv, 8, dtype=torch.bfloat16, device="cuda")
+    at = torch.randint(0, L, (B,), generator=g, device="cuda")
+    scales[torch.arange(B, device="cuda"), at, :, :4] = 0.25
+    q = (8 * torch.randn(B, hq, d, generator=g, device="cuda")).bfloat16()
+    cos, sin = Q.tables(L, d)
+    out, lse = jl.jl_bifocal_decode_q4(q, kc, kc, scales, Q.dev([L] * B, torch.int32), L, 0, w_pre, cos, sin)
+    jl.jl_sync_status()
+    assert bool((out == 0).all())
+    for b in range(B):
+        _, want, _, _ = expect_gpu(q[b], (kc[b], kc[b], scales[b]), L, 0, w_pre)
+        bound = 0.25 * 7.7e-5 * q[b].double().abs().sum(-1) / d**0.5
+        assert bool(((lse[b] - want).abs() <= bound + 2.0**-20 * want.abs()).all())
+
+
 @pytest.mark.parametrize("d,hq,hkv", SHAPES)
 @pytest.mark.parametrize("w0", WINDOWS)
 def test_a_window_off_by_one_would_show(d, hq, hkv, w0):
