@@ -412,7 +412,7 @@ jl_status jl_decode_append_paged(const void* q, const void* k, const void* v, co
  * then scale = bf16(max |x| * fp32(1/7)) over the group and code = round(x / scale), halves to
  * even, clamped to +-7, plus 8.  A scale below 2^-100 is stored as 0 with codes 8; a group
  * that holds a NaN or an infinity gets a NaN scale and reads back as NaN.  The error of a
- * value is at most half a scale (and 2^-9 of the group's largest).
+ * value is at most half a scale.
  *
  * jl_kv_cache_fill_q4, jl_decode_append_q4: the arguments and the error behaviour of
  * jl_kv_cache_fill and jl_decode_append, with the three tensors for the two caches; a row

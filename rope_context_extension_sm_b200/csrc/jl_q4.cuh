@@ -20,10 +20,11 @@
 //   value channel c:  byte (D/16) (c % 8) + c / 16, low four bits if c % 16 < 8, else high
 //
 // Rounding.  scale = bf16(max|x| * fp32(1/7)) (bf16 keeps the range of the inputs, and the codes are
-// formed with the rounded scale, so its 8 bits cost no accuracy beyond a clamp of 2^-9 of a
-// step); code = round-half-even(x / scale) clamped to +-7.  A group whose scale would be
-// below 2^-100 is stored as zeros (the residuals below stay normal numbers), one that holds
-// a NaN or an infinity gets a NaN scale, so it does not turn into finite values.
+// formed with the rounded scale, so its 8 bits cost no accuracy: a largest value past 7 scales is
+// off by 7 * 2^-8 of one, less than a code's rounding); code = round-half-even(x / scale) clamped
+// to +-7.  A group whose scale would be below 2^-100 is stored as zeros (the residuals below stay
+// normal numbers), one that holds a NaN or an infinity gets a NaN scale, so it does not turn
+// into finite values.
 #pragma once
 
 #include "jl_append.cuh"

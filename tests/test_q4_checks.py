@@ -22,5 +22,5 @@ def test_kernel_checks_its_indices(file, kernel):
 def test_the_decode_checks_rows_pages_tables_and_slots():
     text = open(os.path.join(build.CSRC, "jl_decode_q4.cuh")).read()
     checks = " ".join(re.findall(r"JL_CHECK\((.*?)\);", text, re.S))
-    for name in ("cache_stride", "num_pages", "n_tab_rows", "slot0", "c1 < p.n_cta"):
+    for name in ("cache_stride", "num_pages", "n_tab_rows", "slot0", "c0 + count <= p.n_cta"):
         assert name in checks
