@@ -172,11 +172,12 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 // is off by 2.0e-4 of its size from it at every length, beside 1.67e-3 of its own rounding.  A second
 // fp16 number for the rest would double the values' matrix instructions.  So that the products fit
 // fp16 whatever the scales, each head and value group has a factor of its own, a power of two
-// that keeps weight * scale * factor at or below 2^15, where it was 2^7 when it last moved:
-// products down to 2^-20 of the group's largest keep 11 bits, and down to 2^-31 still count.
-// The softmax's reference M is the largest score when it last moved and moves before a weight
-// passes 2^8; a key that has all the weight has a weight of 1 and gives its values exactly.  The factors are taken off the sums at the end.  Sums and outputs
-// are held in fp32.
+// that keeps weight * scale * factor at or below 2^15, where it was 2^6 to 2^7 when it last
+// moved: products down to 2^-20 of the group's largest keep 11 bits, and down to 2^-31 still
+// count.  The softmax's reference M is the largest score when it last moved, or less than an
+// octave above, and moves before a weight passes 2^8; a first key that has all the weight has
+// a weight of 1 and gives its values exactly, ties of their rounding included.  The factors
+// are taken off the sums at the end.  Sums and outputs are held in fp32.
 //
 // The rotations' cos and sin are the same for all heads, so three warps make them once a tile
 // for the whole head block: from the table's row of a run's first key by steps of one position
@@ -812,7 +813,10 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
             for (int x = 4; x < 32; x <<= 1)
 #pragma unroll
               for (int f = 0; f < 5; ++f) top[f] = fmaxf(top[f], __shfl_xor_sync(0xffffffffu, top[f], x));
-            const float now = fmaxf(m[n], top[4]);
+            // M rises by whole octaves, so that the factors can follow exactly; where little of what
+            // was before is left (and at first) to the score itself
+            const float rise = top[4] - m[n];
+            const float now = rise > 24.f ? top[4] : m[n] + ceilf(fmaxf(rise, 0.f));
             const bool first = m[n] == -INFINITY;
             l[n] *= first ? 0.f : ex2_approx(m[n] - now);
 #pragma unroll
@@ -825,8 +829,8 @@ __global__ void __launch_bounds__(kDecodeQ4Threads, 1)
                 // log2 of the weight * scale, before M, whose product is 1: as it was, and from now on
                 const float was = first ? -INFINITY : m[n] - (static_cast<int>(__float_as_uint(fc[z]) >> 23) - 127);
                 const float to = fmaxf(was, top[f] - 7.f);
-                const float up = floorf(fminf(119.f, fmaxf(-119.f, now - to)));
-                by[n][f] = first ? 0.f : ex2_approx(was - now + up);  // at most 1
+                const float up = floorf(fminf(119.f, fmaxf(-119.f, now - to)) + 0.0625f);  // M's own rounding
+                by[n][f] = first ? 0.f : ex2_approx(was - now + up);
                 fc[z] = __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(up)) << 23);
                 most[f] = fmaxf(most[f], fc[z]);
               }

@@ -209,3 +209,62 @@ def test_a_lone_key_gives_its_values(jl, d, hq, hkv):  # noqa: F811
     jl.jl_sync_status()
     want = value_rows(cache[1][:, 0], cache[2][:, 0]).bfloat16().repeat_interleave(hq // hkv, 1)
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("octaves", [0.9, 3.3, 7.7, 30.0])
+@pytest.mark.parametrize("d,hq,hkv", [(128, 16, 1), (64, 4, 1), (128, 8, 2)])
+def test_scores_that_rise_with_the_keys(jl, d, hq, hkv, octaves):  # noqa: F811
+    """Scores that rise by some octaves every 128 keys, value scales that fall as fast, so that every key counts and
+    the references move again and again; a batch that leaves each entry to one CTA or two.  Bounds as above, with the
+    scores' error on top: fp32 scores, up to 700 in units of ln 2 here, to 2^-22 of themselves."""
+    B, L = 150, 128 * max(3, min(40, int(700 / octaves)))
+    g = torch.Generator(device="cuda").manual_seed(97)
+    kc = torch.full((B, L, hkv, d // 2), 0xff, dtype=torch.uint8, device="cuda")  # 7 in every channel
+    vc = uniform_codes(g, B, L, hkv, d // 2)
+    level = torch.arange(L, device="cuda") // 128 * octaves  # of the first head, in octaves
+    q = torch.rand(B, hq, 1, generator=g, device="cuda").mul_(0.05).add_(0.95).expand(B, hq, d).bfloat16()
+    unit = 7 * d**0.5  # the score of a key scale of 1 for a query of ones
+    sc = torch.empty(B, L, hkv, 8, device="cuda").uniform_(0.9, 1.1, generator=g)
+    sc[..., :4] = (level * np.log(2) / unit)[:, None, None]
+    sc[..., 4:] *= torch.exp2(60 - level.clamp(max=150))[:, None, None]
+    sc[..., 5] *= 1e-20
+    sc = sc.bfloat16()
+    tab = torch.ones(L, d // 2, device="cuda")
+    out, lse = jl.jl_bifocal_decode_q4(q, kc, vc, sc, Q.dev([L] * B, torch.int32), L, 0, L, tab, tab)
+    jl.jl_sync_status()
+    for b in (0, 1, B // 2, B - 1):
+        want, want_lse, size, most = expect_gpu(q[b], (kc[b], vc[b], sc[b]), L, 0, L)
+        step = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=2.0**-126))) - 8)
+        slack = (2.0**-11 + 700 * np.log(2) * 2.0**-22) * size + 7 * L * 2.0**-31 * most
+        assert bool(((out[b].double() - want).abs() <= step + slack).all())
+        assert bool(((lse[b] - want_lse).abs() <= 2.0**-21 * want_lse.abs() + 1e-5).all())
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(128, 16, 1), (64, 4, 1), (128, 8, 2)])
+def test_a_group_that_grows_while_scores_rise(jl, d, hq, hkv):  # noqa: F811
+    """Every 128 keys one group's value scales grow by eight octaves, so that references and factors move each time,
+    while scores rise by 0.97 and the other groups' scales fall by as much: their keys count alike to the last, and a
+    factor that lost that part of an octave at every move would round them among subnormals."""
+    B, tiles = 150, 27
+    L = 128 * tiles
+    g = torch.Generator(device="cuda").manual_seed(98)
+    kc = torch.full((B, L, hkv, d // 2), 0xff, dtype=torch.uint8, device="cuda")  # 7 in every channel
+    vc = uniform_codes(g, B, L, hkv, d // 2)
+    tile = torch.arange(L, device="cuda") // 128
+    q = torch.full((B, hq, d), 0.97 * np.log(2) * 128 / (7 * d**0.5), device="cuda").bfloat16()
+    sc = torch.empty(B, L, hkv, 8, device="cuda").uniform_(0.9, 1.1, generator=g)
+    sc[..., :4] = (tile / 128)[:, None, None]  # exact in bf16
+    sc[..., 4:7] *= torch.exp2(-0.97 * tile)[:, None, None]
+    sc[..., 7] *= torch.exp2(-95 + 8.1 * tile)[:, None]
+    sc = sc.bfloat16()
+    tab = torch.ones(L, d // 2, device="cuda")
+    out, _ = jl.jl_bifocal_decode_q4(q, kc, vc, sc, Q.dev([L] * B, torch.int32), L, 0, L, tab, tab)
+    jl.jl_sync_status()
+    for b in (0, B // 2, B - 1):
+        want, _, size, most = expect_gpu(q[b], (kc[b], vc[b], sc[b]), L, 0, L)
+        # beside the largest of a group all keys of the last tiles count, so the root mean square of the
+        # roundings stands for them: six deviations, as in the tests of long outputs above
+        at = slice(0, 3 * d // 4)
+        assert excess(out[b][:, at], want[:, at]) <= 6 * 2.0**-11 / 3**0.5
+        step = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=2.0**-126))) - 8)
+        assert bool(((out[b].double() - want).abs() <= step + (2.0**-11 + 2.0**-15) * size + 7 * L * 2.0**-31 * most).all())
