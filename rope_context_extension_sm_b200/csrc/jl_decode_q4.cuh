@@ -126,14 +126,14 @@ __device__ __forceinline__ Q4Start q4_range(const DecodeQ4Params& p, int lane) {
 //
 // What bounds it.  A row of 128 channels is 144 bytes: 128K keys of eight heads are 151 MB,
 // 23.0 us at the measured 6.56 TB/s.  Beside that stand, for 16 keys of one head (8192 of
-// those a head at 128K), 545 warp instructions in all to expand, weigh and sum 4096 codes and
+// those a head at 128K), 540 warp instructions in all to expand, weigh and sum 4096 codes and
 // to rotate the keys, of which the ALU and the fp16 pipe take two cycles each.  Measured
-// (graph-replayed, 32/8 heads of 128, cold caches): 63.7 us at 128K keys (G = 4), 2.4 TB/s,
-// of which 54 us are per key and 9 for the start, the first loads and the join; without
+// (graph-replayed, 32/8 heads of 128, cold caches): 64.1 us at 128K keys (G = 4), 2.4 TB/s,
+// of which 55 us are per key and 9 for the start, the first loads and the join; without
 // rotation (G = 1) 30 us are per key.  8K keys take 11.2 us.  With the instructions of the
 // keys and values left out, the loads alone stream 128K keys in 21 us.  So the arithmetic
-// bounds it, although no pipe is full: issue slots are 48 % used, the FMA pipe 44 %, the
-// tensor pipe 17 %, DRAM 27 %.  Two warps a scheduler wait for their own results, for one
+// bounds it, although no pipe is full: issue slots are 46 % used, the FMA pipe 43 %, the
+// tensor pipe 16 %, DRAM 28 %.  Two warps a scheduler wait for their own results, for one
 // another's pipes, and (0.5 of a warp at every issue) for instructions to be fetched.
 //
 // Shape.  Eight warps of a CTA take keys; one loads; three make the rotations' factors.  A
